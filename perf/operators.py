@@ -274,7 +274,7 @@ def _run_own(s):
         if way == "forward":
             return moe.moe_dispatch(s["x"], t, s["k"], rows=s["rows"], x_scale=s.get("x_scale"),
                                     rows_scale=s.get("rows_scale"))
-        return moe.moe_dispatch_backward(s["drows"], t, s["k"])
+        return moe.moe_dispatch_backward(s["drows"], t, s["M"], s["k"])
     if way == "forward":
         return moe.moe_combine(s["rows"], s["w"], t, out_dtype=s["out_dtype"])
     drows, dw = moe.moe_combine_backward(s["dout"], s["rows"], s["w"], t, drows=s.get("drows"),
