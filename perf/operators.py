@@ -365,8 +365,8 @@ def _norm_grad_plain(s):
 
 def _e4m3(q):
     """The E4M3 values nearest to float64 q (|q| <= 448), ties to even."""
-    _, e = torch.frexp(q)
-    step = torch.ldexp(torch.ones_like(q), (e - 1).clamp(min=-6) - 3)
+    e = (torch.frexp(q)[1].long() - 1).clamp(min=-6) - 3
+    step = ((e + 1023) << 52).view(torch.float64)   # 2^e; torch.ldexp is not exact
     return torch.round(q / step) * step
 
 
