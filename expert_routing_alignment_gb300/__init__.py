@@ -28,6 +28,7 @@ MOE_EINVAL = 1
 MOE_EUNSUPPORTED = 2
 MOE_ECUDA = 3
 MOE_ERR_BAD_ID = 0x1
+MOE_ERR_BAD_POSITION = 0x4
 
 FMT_FP8_B128 = 1
 FMT_NVFP4_G16 = 2
@@ -38,6 +39,11 @@ PATH_TC = 2
 PATH_SIMT_STAGED = 3
 MOE_ERR_TIMEOUT = 0x2
 MAX_EXPERTS = 1024
+MAX_NORM_HIDDEN = 16384
+DTYPE_BF16 = 1
+DTYPE_F16 = 2
+DTYPE_F32 = 3
+DTYPE_E4M3 = 4
 MAX_ROWS = 128
 MAX_ROWS_TC = 4096   # M admitted on the tensor-core path (FP8 experts)
 TOKEN_FORM_ROWS = 16   # tensor-core path: up to this M, x terms are kept by token
@@ -90,6 +96,7 @@ class _WsView(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 EXPORTS = {
     "moe_version": (ctypes.c_char_p, []),
     "moe_status_string": (ctypes.c_char_p, [_I]),
@@ -113,6 +120,19 @@ EXPORTS = {
                                       _P]),
     "moe_decode_experts": (_I, [ctypes.POINTER(_LayerDesc), _P, _I, _P, _P, ctypes.c_size_t, _P,
                                 _P]),
+    "moe_dispatch": (_I, [_P, _L, _P, _I, _I, _I, _I, _P, _P, _P, _I, _P, _P, _P, _P]),
+    "moe_dispatch_backward": (_I, [_P, _I, _I, _I, _I, _P, _I, _P, _P, _P]),
+    "moe_combine": (_I, [_P, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_combine_backward": (_I, [_P, _L, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P,
+                                  _P]),
+    "moe_topk_softmax_backward": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "moe_add_rmsnorm": (_I, [_P, _L, _P, _L, _P, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P, _P,
+                             _P, _P]),
+    "moe_add_rmsnorm_backward_workspace_bytes": (ctypes.c_size_t, [_I, _I]),
+    "moe_add_rmsnorm_backward": (_I, [_P, _L, _P, _L, _P, _P, _P, _L, _I, _I, _I, _I, _P, _P, _P,
+                                      ctypes.c_size_t, _P]),
+    "moe_decode_block": (_I, [ctypes.POINTER(_LayerDesc), _P, _P, _P, ctypes.c_float, _I, _P, _P,
+                              _P, _P, ctypes.c_size_t, _P, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -448,3 +468,345 @@ def moe_decode_layer_noalloc(layer: LayerDesc, x: torch.Tensor, out: torch.Tenso
     _check("moe_decode_layer_noalloc", load().moe_decode_layer_noalloc(
         ctypes.pointer(layer._struct), _ptr(x), M, _ptr(router_logits), _ptr(topk_ids),
         _ptr(topk_w), _ptr(out), _ptr(err_word), _stream(stream)))
+
+
+# --------------------------------------------------------------------------
+# tokens in expert order and back, the norm ahead of the router, gradients
+# --------------------------------------------------------------------------
+
+_FLOAT = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
+# E4M3 rows: torch's float8 type, or the bytes
+_ROWS = {**_FLOAT, torch.float8_e4m3fn: DTYPE_E4M3, torch.uint8: DTYPE_E4M3}
+
+
+def _on_device(*tensors: Optional[torch.Tensor]) -> None:
+    """The kernels run on the current device: refuse tensors of any other."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        d = t.get_device()
+        if d < 0:
+            raise ValueError("want CUDA tensors")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if d != dev:
+            raise ValueError(f"want tensors of the current device cuda:{dev}, got cuda:{d}")
+
+
+def _kind(name: str, t: torch.Tensor, kinds: dict) -> int:
+    try:
+        return kinds[t.dtype]
+    except KeyError:
+        raise ValueError(f"{name}: unsupported type {t.dtype}") from None
+
+
+def _row_stride(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> int:
+    """The distance of the rows of an input whose rows are dense."""
+    if t.dtype != dtype or tuple(t.shape) != shape or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: want a {dtype} tensor of shape {shape} with dense rows, "
+                         f"got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _empty(shape: tuple, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """A new output: it belongs to the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else \
+            torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _tables(tables: dict, n: int) -> tuple:
+    """(token_to_perm, sorted_token_ids, num_tokens_post_padded, num_rows)."""
+    ttp, sti = tables["token_to_perm"], tables["sorted_token_ids"]
+    ntpp = tables["num_tokens_post_padded"]
+    for name, t, size in (("token_to_perm", ttp, n), ("num_tokens_post_padded", ntpp, 1),
+                          ("sorted_token_ids", sti, None)):
+        if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != 1 or \
+                (size is not None and t.numel() < size):
+            raise ValueError(f"{name}: want a contiguous int32 tensor"
+                             + (f" of {size} elements" if size is not None else ""))
+    return ttp, sti, ntpp, min(sti.numel(), tables.get("max_total", sti.numel()))
+
+
+def _err(err_word: Optional[torch.Tensor]) -> None:
+    if err_word is not None and (err_word.dtype not in (torch.int32, torch.uint32)
+                                 or err_word.numel() < 1):
+        raise ValueError("err_word: want an int32 tensor")
+
+
+def moe_dispatch(x: torch.Tensor, tables: dict, top_k: int, rows: Optional[torch.Tensor] = None,
+                 x_scale: Optional[torch.Tensor] = None,
+                 rows_scale: Optional[torch.Tensor] = None,
+                 err_word: Optional[torch.Tensor] = None, stream=None):
+    """Token rows x [M, H] into expert order by moe_align's tables: rows
+    [max_total, H], zeros in the padding, what was there behind the total
+    (undefined in a new buffer).  E4M3 x (float8_e4m3fn, or the bytes) comes
+    with x_scale fp32 [M, ceil(H / 128)]; then (rows, rows_scale)."""
+    M, H = x.shape
+    kind = _kind("x", x, _ROWS)
+    xs = _row_stride("x", x, x.dtype, (M, H))
+    ttp, sti, ntpp, n_rows = _tables(tables, M * top_k)
+    _err(err_word)
+    _on_device(x, ttp, sti, ntpp, rows, x_scale, rows_scale, err_word)
+    if (kind == DTYPE_E4M3) != (x_scale is not None):
+        raise ValueError("x_scale: E4M3 rows have scales, others none")
+    if rows is None:
+        rows = _empty((n_rows, H), x.dtype, x.device, stream)
+    _dense("rows", rows, x.dtype, (n_rows, H))
+    if x_scale is not None:
+        _dense("x_scale", x_scale, torch.float32, (M, -(-H // 128)))
+        if rows_scale is None:
+            rows_scale = _empty((n_rows, -(-H // 128)), torch.float32, x.device, stream)
+        _dense("rows_scale", rows_scale, torch.float32, (n_rows, -(-H // 128)))
+    elif rows_scale is not None:
+        raise ValueError("rows_scale: E4M3 rows have scales, others none")
+    _check("moe_dispatch", load().moe_dispatch(
+        _ptr(x), xs, _ptr(x_scale), kind, M, top_k, H, _ptr(ttp), _ptr(sti), _ptr(ntpp), n_rows,
+        _ptr(rows), _ptr(rows_scale), _ptr(err_word), _stream(stream)))
+    return rows if x_scale is None else (rows, rows_scale)
+
+
+def moe_dispatch_backward(drows: torch.Tensor, tables: dict, M: int, top_k: int,
+                          dx: Optional[torch.Tensor] = None,
+                          err_word: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of moe_dispatch: dx [M, H] = the sum over a token's slots of
+    drows [max_total, H], fp32, rounded once."""
+    ttp, _, _, n_rows = _tables(tables, M * top_k)
+    kind, H = _kind("drows", drows, _FLOAT), drows.shape[-1]
+    _dense("drows", drows, drows.dtype, (n_rows, H))
+    _err(err_word)
+    _on_device(drows, ttp, dx, err_word)
+    if dx is None:
+        dx = _empty((M, H), drows.dtype, drows.device, stream)
+    _dense("dx", dx, drows.dtype, (M, H))
+    _check("moe_dispatch_backward", load().moe_dispatch_backward(
+        _ptr(drows), kind, M, top_k, H, _ptr(ttp), n_rows, _ptr(dx), _ptr(err_word),
+        _stream(stream)))
+    return dx
+
+
+def moe_combine(rows: torch.Tensor, topk_w: torch.Tensor, tables: dict,
+                out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                err_word: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out [M, H] = sum_j topk_w[t, j] * rows[token_to_perm[t, j]], fp32, j
+    ascending, rounded once to out's type (out_dtype, or rows')."""
+    M, k = topk_w.shape
+    ttp, sti, ntpp, n_rows = _tables(tables, M * k)
+    kind, H = _kind("rows", rows, _FLOAT), rows.shape[-1]
+    _dense("rows", rows, rows.dtype, (n_rows, H))
+    _dense("topk_w", topk_w, torch.float32, (M, k))
+    _err(err_word)
+    _on_device(rows, topk_w, ttp, out, err_word)
+    if out is None:
+        out = _empty((M, H), out_dtype or rows.dtype, rows.device, stream)
+    okind = _kind("out", out, _FLOAT)
+    _dense("out", out, out_dtype or out.dtype, (M, H))
+    _check("moe_combine", load().moe_combine(
+        _ptr(rows), kind, _ptr(topk_w), _ptr(ttp), M, k, H, n_rows, okind, _ptr(out),
+        _ptr(err_word), _stream(stream)))
+    return out
+
+
+def moe_combine_backward(dout: torch.Tensor, rows: Optional[torch.Tensor], topk_w: torch.Tensor,
+                         tables: dict, drows: Optional[torch.Tensor] = None,
+                         dtopk_w: Optional[torch.Tensor] = None, want_drows: bool = True,
+                         want_dtopk_w: bool = True, rows_dtype: Optional[torch.dtype] = None,
+                         err_word: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of moe_combine: (drows [max_total, H], dtopk_w [M, k]), None
+    where it is not wanted.  drows has zeros in the padding and keeps what was
+    there behind the total.  rows may be None when dtopk_w is not wanted: then
+    drows has rows_dtype, or dout's type."""
+    M, k = topk_w.shape
+    H = dout.shape[-1]
+    ttp, sti, ntpp, n_rows = _tables(tables, M * k)
+    okind = _kind("dout", dout, _FLOAT)
+    ds = _row_stride("dout", dout, dout.dtype, (M, H))
+    _dense("topk_w", topk_w, torch.float32, (M, k))
+    if rows is not None:
+        rtype = rows.dtype
+        _dense("rows", rows, rtype, (n_rows, H))
+    elif want_dtopk_w:
+        raise ValueError("rows: needed for dtopk_w")
+    else:
+        rtype = rows_dtype or (drows.dtype if drows is not None else dout.dtype)
+    if not want_drows and not want_dtopk_w:
+        raise ValueError("neither drows nor dtopk_w is wanted")
+    if rtype not in _FLOAT:
+        raise ValueError(f"rows: unsupported type {rtype}")
+    _err(err_word)
+    _on_device(dout, rows, topk_w, ttp, sti, ntpp, drows, dtopk_w, err_word)
+    if not want_drows:
+        drows = None
+    else:
+        if drows is None:
+            drows = _empty((n_rows, H), rtype, dout.device, stream)
+        _dense("drows", drows, rtype, (n_rows, H))
+    if not want_dtopk_w:
+        dtopk_w = None
+    else:
+        if dtopk_w is None:
+            dtopk_w = _empty((M, k), torch.float32, dout.device, stream)
+        _dense("dtopk_w", dtopk_w, torch.float32, (M, k))
+    _check("moe_combine_backward", load().moe_combine_backward(
+        _ptr(dout), ds, okind, _ptr(rows), _FLOAT[rtype], _ptr(topk_w), _ptr(ttp), _ptr(sti),
+        _ptr(ntpp), M, k, H, n_rows, _ptr(drows), _ptr(dtopk_w), _ptr(err_word),
+        _stream(stream)))
+    return drows, dtopk_w
+
+
+def moe_topk_softmax_backward(topk_ids: torch.Tensor, topk_w: torch.Tensor,
+                              dtopk_w: torch.Tensor, num_experts: int,
+                              dlogits: Optional[torch.Tensor] = None,
+                              err_word: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """Gradient of moe_topk_softmax: dlogits fp32 [M, E] from the weights'
+    gradients dtopk_w [M, k]; 0 for every logit that was not selected."""
+    M, k = topk_w.shape
+    _dense("topk_ids", topk_ids, torch.int32, (M, k))
+    _dense("topk_w", topk_w, torch.float32, (M, k))
+    _dense("dtopk_w", dtopk_w, torch.float32, (M, k))
+    _err(err_word)
+    _on_device(topk_ids, topk_w, dtopk_w, dlogits, err_word)
+    if dlogits is None:
+        dlogits = _empty((M, num_experts), torch.float32, topk_w.device, stream)
+    _dense("dlogits", dlogits, torch.float32, (M, num_experts))
+    _check("moe_topk_softmax_backward", load().moe_topk_softmax_backward(
+        _ptr(topk_ids), _ptr(topk_w), _ptr(dtopk_w), M, num_experts, k, _ptr(dlogits),
+        _ptr(err_word), _stream(stream)))
+    return dlogits
+
+
+def alloc_add_rmsnorm_outputs(x: torch.Tensor, want: Sequence[str], stream=None) -> dict:
+    """Buffers for moe_add_rmsnorm: "out", "sum" [M, H] of x's type, "codes"
+    float8_e4m3fn [M, H] and "scale" fp32 [M, ceil(H / 128)], "rstd" fp32 [M]."""
+    M, H = x.shape
+    made = {}
+    for name in want:
+        if name in ("out", "sum"):
+            shape, dtype = (M, H), x.dtype
+        elif name == "codes":
+            shape, dtype = (M, H), torch.float8_e4m3fn
+        elif name == "scale":
+            shape, dtype = (M, -(-H // 128)), torch.float32
+        elif name == "rstd":
+            shape, dtype = (M,), torch.float32
+        else:
+            raise ValueError(f"want: no output {name!r}")
+        made[name] = _empty(shape, dtype, x.device, stream)
+    return made
+
+
+def moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                    residual: Optional[torch.Tensor] = None, want: Sequence[str] = ("out",),
+                    out: Optional[dict] = None, stream=None) -> dict:
+    """sum = x + residual (rounded to x's type), out = sum * rstd * weight with
+    rstd = 1 / sqrt(mean(sum^2) + eps) by rows; "codes" and "scale" are out in
+    E4M3 with a scale per 128 columns.  Writes the buffers of ``out``, or new
+    ones for the outputs in ``want``, and returns them by name."""
+    M, H = x.shape
+    kind, wkind = _kind("x", x, _FLOAT), _kind("weight", weight, _FLOAT)
+    xs = _row_stride("x", x, x.dtype, (M, H))
+    rs = 0 if residual is None else _row_stride("residual", residual, x.dtype, (M, H))
+    _dense("weight", weight, weight.dtype, (H,))
+    _on_device(x, weight, residual)
+    if out is None:
+        out = alloc_add_rmsnorm_outputs(x, want, stream)
+    else:
+        _on_device(*out.values())
+    shapes = {"out": (M, H), "sum": (M, H), "codes": (M, H), "scale": (M, -(-H // 128)),
+              "rstd": (M,)}
+    for name, t in out.items():
+        if name not in shapes:
+            raise ValueError(f"out: no output {name!r}")
+        if name == "codes":
+            dtype = torch.uint8 if t.dtype == torch.uint8 else torch.float8_e4m3fn
+        else:
+            dtype = torch.float32 if name in ("scale", "rstd") else x.dtype
+        _dense(name, t, dtype, shapes[name])
+    g = out.get
+    _check("moe_add_rmsnorm", load().moe_add_rmsnorm(
+        _ptr(x), xs, _ptr(residual), rs, _ptr(weight), kind, wkind, M, H, eps, _ptr(g("sum")),
+        _ptr(g("out")), _ptr(g("codes")), _ptr(g("scale")), _ptr(g("rstd")), _stream(stream)))
+    return out
+
+
+def add_rmsnorm_backward_workspace_bytes(M: int, hidden: int) -> int:
+    nbytes = load().moe_add_rmsnorm_backward_workspace_bytes(M, hidden)
+    if nbytes == 0:
+        raise MoeError("moe_add_rmsnorm_backward_workspace_bytes", MOE_EINVAL)
+    return nbytes
+
+
+def moe_add_rmsnorm_backward(dout: torch.Tensor, sum: torch.Tensor, weight: torch.Tensor,
+                             rstd: torch.Tensor, dsum: Optional[torch.Tensor] = None,
+                             dx: Optional[torch.Tensor] = None,
+                             dweight: Optional[torch.Tensor] = None, want_dweight: bool = True,
+                             workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of moe_add_rmsnorm from its "sum" and "rstd": (dx [M, H] of
+    dout's type, dweight fp32 [H] or None).  dx is the gradient of x and of
+    residual; dsum is the gradient that reaches "sum" from elsewhere.  The
+    weight gradient needs a workspace (a new one when None)."""
+    M, H = dout.shape
+    kind, wkind = _kind("dout", dout, _FLOAT), _kind("weight", weight, _FLOAT)
+    ds = _row_stride("dout", dout, dout.dtype, (M, H))
+    ss = _row_stride("sum", sum, dout.dtype, (M, H))
+    es = 0 if dsum is None else _row_stride("dsum", dsum, dout.dtype, (M, H))
+    _dense("weight", weight, weight.dtype, (H,))
+    _dense("rstd", rstd, torch.float32, (M,))
+    _on_device(dout, sum, weight, rstd, dsum, dx, dweight, workspace)
+    if dx is None:
+        dx = _empty((M, H), dout.dtype, dout.device, stream)
+    _dense("dx", dx, dout.dtype, (M, H))
+    nbytes = 0
+    if not want_dweight:
+        dweight = workspace = None
+    else:
+        if dweight is None:
+            dweight = _empty((H,), torch.float32, dout.device, stream)
+        _dense("dweight", dweight, torch.float32, (H,))
+        if workspace is None:
+            nbytes = add_rmsnorm_backward_workspace_bytes(M, H)
+            workspace = _empty((nbytes,), torch.uint8, dout.device, stream)
+        else:
+            if not workspace.is_contiguous():
+                raise ValueError("workspace: want a contiguous tensor")
+            nbytes = workspace.numel() * workspace.element_size()
+    _check("moe_add_rmsnorm_backward", load().moe_add_rmsnorm_backward(
+        _ptr(dout), ds, _ptr(sum), ss, _ptr(weight), _ptr(rstd), _ptr(dsum), es, kind, wkind, M,
+        H, _ptr(dx), _ptr(dweight), _ptr(workspace), nbytes, _stream(stream)))
+    return dx, dweight
+
+
+def moe_decode_block(layer: LayerDesc, x: torch.Tensor, residual: Optional[torch.Tensor],
+                     norm_weight: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor,
+                     eps: float = 1e-6, sum_out: Optional[torch.Tensor] = None,
+                     normed: Optional[torch.Tensor] = None,
+                     err_word: Optional[torch.Tensor] = None, stream=None):
+    """The expert half of a block: sum = x + residual, normed = its RMS norm,
+    out = moe_decode_layer(normed) with the layer's router weights.  Returns
+    (sum, normed); sum_out may be residual's own buffer."""
+    M, H = x.shape
+    bf16 = torch.bfloat16
+    if H != layer.routed.hidden:
+        raise ValueError(f"x: want rows of {layer.routed.hidden}, got {H}")
+    if sum_out is None:
+        sum_out = _empty((M, H), bf16, x.device, stream)
+    if normed is None:
+        normed = _empty((M, H), bf16, x.device, stream)
+    for name, t in (("x", x), ("residual", residual), ("out", out), ("sum_out", sum_out),
+                    ("normed", normed)):
+        if t is not None:
+            _dense(name, t, bf16, (M, H))
+    _dense("norm_weight", norm_weight, bf16, (H,))
+    _err(err_word)
+    _on_device(x, residual, norm_weight, out, workspace, sum_out, normed, err_word)
+    _check("moe_decode_block", load().moe_decode_block(
+        ctypes.pointer(layer._struct), _ptr(x), _ptr(residual), _ptr(norm_weight), eps, M,
+        _ptr(sum_out), _ptr(normed), _ptr(out), _ptr(workspace), workspace.numel(),
+        _ptr(err_word), _stream(stream)))
+    return sum_out, normed

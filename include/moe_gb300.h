@@ -50,6 +50,7 @@ extern "C" {
 /* ---- device error bits, ORed into *err_word ----------------------------- */
 #define MOE_ERR_BAD_ID 0x1u   /* an expert id outside [0, E): slot skipped */
 #define MOE_ERR_TIMEOUT 0x2u  /* a bounded pipeline wait gave up: outputs invalid */
+#define MOE_ERR_BAD_POSITION 0x4u /* a sorted position outside the rows: slot skipped */
 
 /* ---- formats and paths -------------------------------------------------- */
 #define MOE_FMT_FP8_B128 1  /* E4M3 codes, fp32 scale per 128x128 block      */
@@ -59,6 +60,13 @@ extern "C" {
  * up in NVFP4_G16, the down projection in FP8_B128.  hidden and inter must be
  * multiples of 128. */
 #define MOE_FMT_NVFP4_GATE_UP 3
+
+/* Storage types of token and expert rows (moe_dispatch, moe_combine,
+ * moe_add_rmsnorm and their gradients). */
+#define MOE_DTYPE_BF16 1
+#define MOE_DTYPE_F16 2
+#define MOE_DTYPE_F32 3
+#define MOE_DTYPE_E4M3 4    /* one byte; a float scale per row and 128 columns  */
 
 #define MOE_PATH_AUTO 0     /* chosen per shape class (never per routing)    */
 #define MOE_PATH_SIMT 1     /* CUDA-core kernels, in-register dequant         */
@@ -72,6 +80,8 @@ extern "C" {
 #define MOE_MAX_ROWS 128          /* M the expert kernels and layer admit     */
 #define MOE_MAX_ROWS_TC 4096      /* M the layer admits on the tensor-core path
                                      (prefill-sized batches of FP8 experts)     */
+
+#define MOE_MAX_NORM_HIDDEN 16384 /* hidden the RMS norm admits                 */
 
 /* One projection of all experts of a set.  Layout for `rows` x `cols`
  * (gate/up: rows = inter, cols = hidden; down: rows = hidden, cols = inter),
@@ -420,6 +430,172 @@ int moe_decode_layer_noalloc(const moe_layer_desc *layer, const uint16_t *x, int
                              const float *router_logits, const int32_t *topk_ids,
                              const float *topk_w, uint16_t *out, uint32_t *err_word,
                              void *stream);
+
+/* ---- tokens in expert order, and back ------------------------------------ */
+
+/* Conventions of this section and the next.
+ *  - token_to_perm, sorted_token_ids and num_tokens_post_padded are
+ *    moe_align's tables (a layer call's workspace holds them too); num_rows is
+ *    their max_total, the rows every expert-order buffer has.  A slot whose
+ *    token_to_perm is -1 is skipped: it reads and writes nothing.  Any other
+ *    value outside [0, num_rows) is skipped too and reported as
+ *    MOE_ERR_BAD_POSITION.
+ *  - Of an expert-order output, the rows of slots are written; padding rows
+ *    below the total (num_tokens_post_padded) are set to zero, so that a
+ *    grouped product over whole blocks reads no garbage; rows at or past the
+ *    total stay as they were.  Padding rows of inputs are never read.
+ *  - M = 0 is valid.  1 <= top_k <= 32, M * top_k <= MOE_MAX_SLOTS, any
+ *    hidden >= 1: rows that are whole 16-byte pieces (16-byte aligned, hidden a
+ *    multiple of 8) take the fast path, others are served element by element.
+ *  - A *_stride is the distance of the rows of an input in elements, >= 0 (0:
+ *    one row for all).  Outputs and expert-order buffers are dense, and
+ *    overlap no input unless stated.
+ *  - Results are bit-deterministic, and a row's bits do not depend on M.
+ *  - Errors: MOE_EINVAL (NULL, negative sizes or strides, unknown type, a
+ *    pointer not aligned to its elements), MOE_EUNSUPPORTED (top_k, M * top_k,
+ *    or a pair of types that is not listed). */
+
+/* Token rows into expert order ("fp8_moe_grouped.rs": the sorted rows that the
+ * grouped launchers of moe_fp8_grouped_sort's tables work on):
+ *   rows[token_to_perm[t*top_k+j]] = x[t]
+ * for MOE_DTYPE_BF16, _F16, _F32 or _E4M3.  E4M3 rows come with their scales,
+ * x_scale [M][ceil(hidden/128)] dense, which go to rows_scale
+ * [num_rows][ceil(hidden/128)] the same way (both NULL for the other types).
+ *   x [M] rows x_stride apart; rows out [num_rows][hidden]. */
+int moe_dispatch(const void *x, int64_t x_stride, const float *x_scale, int dtype,
+                 int M, int top_k, int hidden, const int32_t *token_to_perm,
+                 const int32_t *sorted_token_ids,
+                 const int32_t *num_tokens_post_padded, int num_rows, void *rows,
+                 float *rows_scale, uint32_t *err_word, void *stream);
+
+/* Gradient of moe_dispatch (16- and 32-bit types):
+ *   dx[t] = sum_j drows[token_to_perm[t*top_k+j]]
+ * in fp32, j ascending, rounded once; a token of skipped slots alone gets 0.
+ *   drows [num_rows][hidden]; dx out [M][hidden], both of type dtype. */
+int moe_dispatch_backward(const void *drows, int dtype, int M, int top_k,
+                          int hidden, const int32_t *token_to_perm, int num_rows,
+                          void *dx, uint32_t *err_word, void *stream);
+
+/* Expert rows back to token order with the routing weights applied
+ * ("fp8_moe_grouped.rs", moe_weighted_sum_blend_fp8_grouped; moe_blend is the
+ * layer's form of it, with fp32 rows and a shared expert):
+ *   out[t] = sum_j topk_w[t][j] * rows[token_to_perm[t*top_k+j]]
+ * in fp32, j ascending, rounded once; a token of skipped slots alone gets 0.
+ * Types (rows, out): (BF16, BF16), (F16, F16), (F32, F32), (F32, BF16),
+ * (F32, F16).
+ *   rows [num_rows][hidden]; topk_w [M][top_k]; out [M][hidden]. */
+int moe_combine(const void *rows, int rows_dtype, const float *topk_w,
+                const int32_t *token_to_perm, int M, int top_k, int hidden,
+                int num_rows, int out_dtype, void *out, uint32_t *err_word,
+                void *stream);
+
+/* Gradient of moe_combine, the same pairs of types:
+ *   drows[token_to_perm[t*top_k+j]] = topk_w[t][j] * dout[t]   (rounded once)
+ *   dtopk_w[t][j] = sum_c dout[t][c] * rows[token_to_perm[t*top_k+j]][c]
+ * in fp32; 0 for a skipped slot.  Either output may be NULL (not both):
+ * without dtopk_w, rows may be NULL; without drows, topk_w, sorted_token_ids
+ * and num_tokens_post_padded may.  With the rows that a moe_decode_layer call
+ * leaves in its workspace (y, fp32) dtopk_w is the gradient of the layer's
+ * routing weights.
+ *   dout [M] rows dout_stride apart, of out_dtype; drows out
+ *   [num_rows][hidden] of rows_dtype; dtopk_w out [M][top_k]. */
+int moe_combine_backward(const void *dout, int64_t dout_stride, int out_dtype,
+                         const void *rows, int rows_dtype, const float *topk_w,
+                         const int32_t *token_to_perm,
+                         const int32_t *sorted_token_ids,
+                         const int32_t *num_tokens_post_padded, int M, int top_k,
+                         int hidden, int num_rows, void *drows, float *dtopk_w,
+                         uint32_t *err_word, void *stream);
+
+/* Gradient of moe_topk_softmax: with w the weights of a row's selected logits,
+ *   dlogits[t][topk_ids[t][j]] = w_j * (dtopk_w[t][j] - sum_i w_i dtopk_w[t][i])
+ * in fp32, every other logit's gradient 0 (the selection itself has none).  An
+ * id that stands more than once in a row gets the sum of its slots.  An id
+ * outside [0, num_experts) is skipped (its weight still counts in the sum) and
+ * reported as MOE_ERR_BAD_ID.  M = 0 is valid.
+ *   topk_ids [M][top_k]; topk_w, dtopk_w [M][top_k]; dlogits out
+ *   [M][num_experts], written whole.
+ * Errors: as moe_topk_softmax; MOE_EINVAL also for misaligned pointers. */
+int moe_topk_softmax_backward(const int32_t *topk_ids, const float *topk_w,
+                              const float *dtopk_w, int M, int num_experts,
+                              int top_k, float *dlogits, uint32_t *err_word,
+                              void *stream);
+
+/* ---- residual addition and RMS norm -------------------------------------- */
+
+/* The step ahead of the router in a block of residual layers (the pages have
+ * no counterpart: their layer takes normed rows).  Per row, in fp32:
+ *   s    = T(x + residual)           (residual NULL: s = x)
+ *   rstd = 1 / sqrt(mean(s^2) + eps)
+ *   out  = T(s * rstd * weight)
+ * T rounds to the rows' type; the sum is normalised as it is stored.  And for
+ * products of E4M3 rows, by blocks of 128 columns (the last one may be
+ * shorter), from the unrounded v = s * rstd * weight:
+ *   out_scale = max(max|v| / 448, 2^-126),  out_codes = e4m3(v / out_scale)
+ * rounded to nearest, ties to even, and saturated; a block with a NaN gets a
+ * NaN scale.  The squares' mean and the products |s * weight| * 448 must stay
+ * finite in fp32.
+ * Types: rows BF16, F16 or F32; weight of the rows' type or F32.
+ *   x, residual: M rows, *_stride apart; weight [hidden]; sum_out, out
+ *   [M][hidden]; out_codes [M][hidden] bytes with out_scale
+ *   [M][ceil(hidden/128)] float (both or neither); rstd [M] float.  Every
+ *   output may be NULL, not all of them.  sum_out or out may be x's or
+ *   residual's own buffer when that input is dense (stride = hidden).
+ * M = 0 is valid; any hidden from 1 to MOE_MAX_NORM_HIDDEN, whole 16-byte
+ * pieces fast as above; a row's bits do not depend on M.
+ * Errors: MOE_EINVAL (NULL, sizes, strides, eps negative or not finite, one of
+ * codes and scale alone, a strided input shared with an output, misaligned),
+ * MOE_EUNSUPPORTED (hidden, types). */
+int moe_add_rmsnorm(const void *x, int64_t x_stride, const void *residual,
+                    int64_t residual_stride, const void *weight, int dtype,
+                    int weight_dtype, int M, int hidden, float eps, void *sum_out,
+                    void *out, uint8_t *out_codes, float *out_scale, float *rstd,
+                    void *stream);
+
+/* Host only.  Workspace bytes moe_add_rmsnorm_backward needs for a weight
+ * gradient (0: sizes it would refuse). */
+size_t moe_add_rmsnorm_backward_workspace_bytes(int M, int hidden);
+
+/* Gradient of moe_add_rmsnorm.  With sum and rstd as the forward call left
+ * them, xh = sum * rstd, g = dout * weight, in fp32:
+ *   dx      = T(rstd * (g - xh * mean(g * xh)) + dsum)
+ *   dweight = sum over rows of dout * xh      (fp32, a fixed order)
+ * dx is the gradient of x and of residual alike.  dsum, the gradient that
+ * reaches sum_out from elsewhere (the residual stream), may be NULL; dweight
+ * may be NULL (then no workspace is used).  M = 0 is valid: dweight = 0.
+ *   dout, sum, dsum: M rows, *_stride apart, of type dtype; weight [hidden];
+ *   rstd [M]; dx out [M][hidden], which may be dout's, sum's or dsum's own
+ *   buffer when that input is dense; dweight out [hidden] float.
+ *   workspace: device, 16-byte aligned, at least
+ *   moe_add_rmsnorm_backward_workspace_bytes(M, hidden); it needs no clearing
+ *   and is used only until the call's work is done: calls that overlap on the
+ *   GPU need one each.
+ * Errors: as moe_add_rmsnorm; MOE_EINVAL for a missing or short workspace. */
+int moe_add_rmsnorm_backward(const void *dout, int64_t dout_stride,
+                             const void *sum, int64_t sum_stride,
+                             const void *weight, const float *rstd,
+                             const void *dsum, int64_t dsum_stride, int dtype,
+                             int weight_dtype, int M, int hidden, void *dx,
+                             float *dweight, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* The expert half of a block: moe_add_rmsnorm on bf16 rows, then
+ * moe_decode_layer with the normed rows as its hidden input (the layer needs
+ * router_weight), enqueued on one stream:
+ *   sum_out = x + residual, normed = its norm, out = layer(normed).
+ * out is the layer's output alone: the next block's addition takes it as x
+ * and sum_out as residual.
+ *   x, residual (NULL: sum_out = x), sum_out, normed, out [M][hidden] bf16
+ *   bits, dense; normed and out aligned as moe_decode_layer's x and out.
+ *   sum_out may be residual's or x's buffer; sum_out, normed and out are three
+ *   different buffers.  Workspace rules and shape admission are
+ *   moe_decode_layer's (hidden up to MOE_MAX_NORM_HIDDEN).
+ * Errors: as the two calls; nothing is launched then. */
+int moe_decode_block(const moe_layer_desc *layer, const uint16_t *x,
+                     const uint16_t *residual, const uint16_t *norm_weight,
+                     float eps, int M, uint16_t *sum_out, uint16_t *normed,
+                     uint16_t *out, void *workspace, size_t workspace_bytes,
+                     uint32_t *err_word, void *stream);
 
 #ifdef __cplusplus
 }
