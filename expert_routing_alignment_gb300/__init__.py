@@ -39,7 +39,7 @@ PATH_TC = 2
 PATH_SIMT_STAGED = 3
 MOE_ERR_TIMEOUT = 0x2
 MAX_EXPERTS = 1024
-MAX_NORM_HIDDEN = 16384
+MAX_ROW_HIDDEN = 16384
 DTYPE_BF16 = 1
 DTYPE_F16 = 2
 DTYPE_F32 = 3
@@ -478,65 +478,84 @@ _FLOAT = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: D
 # E4M3 rows: torch's float8 type, or the bytes
 _ROWS = {**_FLOAT, torch.float8_e4m3fn: DTYPE_E4M3, torch.uint8: DTYPE_E4M3}
 
+# These wrappers stand in front of kernels of a few microseconds, so they pass
+# plain addresses, check each tensor once and ask for the current stream's
+# handle directly (a torch.cuda.Stream object costs more than the launch).
 
-def _on_device(*tensors: Optional[torch.Tensor]) -> None:
+
+def _on_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
     """The kernels run on the current device: refuse tensors of any other."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        d = t.get_device()
-        if d < 0:
-            raise ValueError("want CUDA tensors")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if d != dev:
-            raise ValueError(f"want tensors of the current device cuda:{dev}, got cuda:{d}")
+    dev = first.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"want CUDA tensors of the current device, got one on {first.device}")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"want tensors on one device, got {first.device} and {t.device}")
+    return dev
+
+
+def _handle(stream, dev: int) -> int:
+    """The cudaStream_t of a stream argument; None: the device's current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _kind(name: str, t: torch.Tensor, kinds: dict) -> int:
-    try:
-        return kinds[t.dtype]
-    except KeyError:
-        raise ValueError(f"{name}: unsupported type {t.dtype}") from None
+    kind = kinds.get(t.dtype)
+    if kind is None:
+        raise ValueError(f"{name}: unsupported type {t.dtype}")
+    return kind
+
+
+def _at(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> int:
+    """The address of a plain row-major buffer; anything else is refused."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: want a contiguous {dtype} tensor of shape {shape}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _row_stride(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> int:
     """The distance of the rows of an input whose rows are dense."""
-    if t.dtype != dtype or tuple(t.shape) != shape or (shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: want a {dtype} tensor of shape {shape} with dense rows, "
-                         f"got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
-    return t.stride(0) if shape[0] > 1 else shape[1]
+    if t.dtype is dtype and t.shape == shape:
+        s0, s1 = t.stride()
+        if s1 == 1 or shape[1] == 1:
+            return s0 if shape[0] > 1 else shape[1]
+    raise ValueError(f"{name}: want a {dtype} tensor of shape {shape} with dense rows, "
+                     f"got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
 
 
-def _empty(shape: tuple, dtype: torch.dtype, device, stream) -> torch.Tensor:
+def _empty(shape: tuple, dtype: torch.dtype, dev: int, stream) -> torch.Tensor:
     """A new output: it belongs to the stream that the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else \
             torch.cuda.default_stream()
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _tables(tables: dict, n: int) -> tuple:
-    """(token_to_perm, sorted_token_ids, num_tokens_post_padded, num_rows)."""
-    ttp, sti = tables["token_to_perm"], tables["sorted_token_ids"]
-    ntpp = tables["num_tokens_post_padded"]
-    for name, t, size in (("token_to_perm", ttp, n), ("num_tokens_post_padded", ntpp, 1),
-                          ("sorted_token_ids", sti, None)):
-        if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != 1 or \
-                (size is not None and t.numel() < size):
-            raise ValueError(f"{name}: want a contiguous int32 tensor"
-                             + (f" of {size} elements" if size is not None else ""))
-    return ttp, sti, ntpp, min(sti.numel(), tables.get("max_total", sti.numel()))
+def _table(name: str, t: torch.Tensor, least: int) -> int:
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() < least or not t.is_contiguous():
+        raise ValueError(f"{name}: want a contiguous int32 tensor of at least {least} elements, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
 
 
-def _err(err_word: Optional[torch.Tensor]) -> None:
-    if err_word is not None and (err_word.dtype not in (torch.int32, torch.uint32)
-                                 or err_word.numel() < 1):
+def _num_rows(tables: dict) -> int:
+    """Rows of the expert-order buffers: the tables' max_total."""
+    n = tables["sorted_token_ids"].numel()
+    return min(n, tables.get("max_total", n))
+
+
+def _err(err_word: Optional[torch.Tensor]):
+    if err_word is None:
+        return None
+    if err_word.dtype not in (torch.int32, torch.uint32) or err_word.numel() < 1:
         raise ValueError("err_word: want an int32 tensor")
+    return err_word.data_ptr()
 
 
 def moe_dispatch(x: torch.Tensor, tables: dict, top_k: int, rows: Optional[torch.Tensor] = None,
@@ -548,26 +567,32 @@ def moe_dispatch(x: torch.Tensor, tables: dict, top_k: int, rows: Optional[torch
     (undefined in a new buffer).  E4M3 x (float8_e4m3fn, or the bytes) comes
     with x_scale fp32 [M, ceil(H / 128)]; then (rows, rows_scale)."""
     M, H = x.shape
-    kind = _kind("x", x, _ROWS)
-    xs = _row_stride("x", x, x.dtype, (M, H))
-    ttp, sti, ntpp, n_rows = _tables(tables, M * top_k)
-    _err(err_word)
-    _on_device(x, ttp, sti, ntpp, rows, x_scale, rows_scale, err_word)
-    if (kind == DTYPE_E4M3) != (x_scale is not None):
-        raise ValueError("x_scale: E4M3 rows have scales, others none")
-    if rows is None:
-        rows = _empty((n_rows, H), x.dtype, x.device, stream)
-    _dense("rows", rows, x.dtype, (n_rows, H))
+    dtype, kind = x.dtype, _kind("x", x, _ROWS)
+    xs = _row_stride("x", x, dtype, (M, H))
+    ttp, sti = tables["token_to_perm"], tables["sorted_token_ids"]
+    total, n_rows = tables["num_tokens_post_padded"], _num_rows(tables)
+    t_at, s_at = _table("token_to_perm", ttp, M * top_k), _table("sorted_token_ids", sti, n_rows)
+    n_at, e_at = _table("num_tokens_post_padded", total, 1), _err(err_word)
+    if (kind == DTYPE_E4M3) != (x_scale is not None) or (rows_scale is not None
+                                                         and x_scale is None):
+        raise ValueError("x_scale, rows_scale: E4M3 rows have scales, others none")
+    r_at = None if rows is None else _at("rows", rows, dtype, (n_rows, H))
+    xs_at = rs_at = None
     if x_scale is not None:
-        _dense("x_scale", x_scale, torch.float32, (M, -(-H // 128)))
-        if rows_scale is None:
-            rows_scale = _empty((n_rows, -(-H // 128)), torch.float32, x.device, stream)
-        _dense("rows_scale", rows_scale, torch.float32, (n_rows, -(-H // 128)))
-    elif rows_scale is not None:
-        raise ValueError("rows_scale: E4M3 rows have scales, others none")
+        blocks = -(-H // 128)
+        xs_at = _at("x_scale", x_scale, torch.float32, (M, blocks))
+        if rows_scale is not None:
+            rs_at = _at("rows_scale", rows_scale, torch.float32, (n_rows, blocks))
+    dev = _on_device(x, ttp, sti, total, rows, x_scale, rows_scale, err_word)
+    if r_at is None:
+        rows = _empty((n_rows, H), dtype, dev, stream)
+        r_at = rows.data_ptr()
+    if xs_at is not None and rs_at is None:
+        rows_scale = _empty((n_rows, blocks), torch.float32, dev, stream)
+        rs_at = rows_scale.data_ptr()
     _check("moe_dispatch", load().moe_dispatch(
-        _ptr(x), xs, _ptr(x_scale), kind, M, top_k, H, _ptr(ttp), _ptr(sti), _ptr(ntpp), n_rows,
-        _ptr(rows), _ptr(rows_scale), _ptr(err_word), _stream(stream)))
+        x.data_ptr(), xs, xs_at, kind, M, top_k, H, t_at, s_at, n_at, n_rows, r_at, rs_at, e_at,
+        _handle(stream, dev)))
     return rows if x_scale is None else (rows, rows_scale)
 
 
@@ -576,17 +601,17 @@ def moe_dispatch_backward(drows: torch.Tensor, tables: dict, M: int, top_k: int,
                           err_word: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gradient of moe_dispatch: dx [M, H] = the sum over a token's slots of
     drows [max_total, H], fp32, rounded once."""
-    ttp, _, _, n_rows = _tables(tables, M * top_k)
-    kind, H = _kind("drows", drows, _FLOAT), drows.shape[-1]
-    _dense("drows", drows, drows.dtype, (n_rows, H))
-    _err(err_word)
-    _on_device(drows, ttp, dx, err_word)
-    if dx is None:
-        dx = _empty((M, H), drows.dtype, drows.device, stream)
-    _dense("dx", dx, drows.dtype, (M, H))
+    dtype, kind, H = drows.dtype, _kind("drows", drows, _FLOAT), drows.shape[-1]
+    ttp, n_rows = tables["token_to_perm"], _num_rows(tables)
+    t_at, e_at = _table("token_to_perm", ttp, M * top_k), _err(err_word)
+    r_at = _at("drows", drows, dtype, (n_rows, H))
+    x_at = None if dx is None else _at("dx", dx, dtype, (M, H))
+    dev = _on_device(drows, ttp, dx, err_word)
+    if x_at is None:
+        dx = _empty((M, H), dtype, dev, stream)
+        x_at = dx.data_ptr()
     _check("moe_dispatch_backward", load().moe_dispatch_backward(
-        _ptr(drows), kind, M, top_k, H, _ptr(ttp), n_rows, _ptr(dx), _ptr(err_word),
-        _stream(stream)))
+        r_at, kind, M, top_k, H, t_at, n_rows, x_at, e_at, _handle(stream, dev)))
     return dx
 
 
@@ -596,19 +621,22 @@ def moe_combine(rows: torch.Tensor, topk_w: torch.Tensor, tables: dict,
     """out [M, H] = sum_j topk_w[t, j] * rows[token_to_perm[t, j]], fp32, j
     ascending, rounded once to out's type (out_dtype, or rows')."""
     M, k = topk_w.shape
-    ttp, sti, ntpp, n_rows = _tables(tables, M * k)
     kind, H = _kind("rows", rows, _FLOAT), rows.shape[-1]
-    _dense("rows", rows, rows.dtype, (n_rows, H))
-    _dense("topk_w", topk_w, torch.float32, (M, k))
-    _err(err_word)
-    _on_device(rows, topk_w, ttp, out, err_word)
-    if out is None:
-        out = _empty((M, H), out_dtype or rows.dtype, rows.device, stream)
-    okind = _kind("out", out, _FLOAT)
-    _dense("out", out, out_dtype or out.dtype, (M, H))
+    ttp, n_rows = tables["token_to_perm"], _num_rows(tables)
+    t_at, e_at = _table("token_to_perm", ttp, M * k), _err(err_word)
+    r_at = _at("rows", rows, rows.dtype, (n_rows, H))
+    w_at = _at("topk_w", topk_w, torch.float32, (M, k))
+    otype = out_dtype or (rows.dtype if out is None else out.dtype)
+    okind = _FLOAT.get(otype)
+    if okind is None:
+        raise ValueError(f"out: unsupported type {otype}")
+    o_at = None if out is None else _at("out", out, otype, (M, H))
+    dev = _on_device(rows, topk_w, ttp, out, err_word)
+    if o_at is None:
+        out = _empty((M, H), otype, dev, stream)
+        o_at = out.data_ptr()
     _check("moe_combine", load().moe_combine(
-        _ptr(rows), kind, _ptr(topk_w), _ptr(ttp), M, k, H, n_rows, okind, _ptr(out),
-        _ptr(err_word), _stream(stream)))
+        r_at, kind, w_at, t_at, M, k, H, n_rows, okind, o_at, e_at, _handle(stream, dev)))
     return out
 
 
@@ -622,40 +650,42 @@ def moe_combine_backward(dout: torch.Tensor, rows: Optional[torch.Tensor], topk_
     there behind the total.  rows may be None when dtopk_w is not wanted: then
     drows has rows_dtype, or dout's type."""
     M, k = topk_w.shape
-    H = dout.shape[-1]
-    ttp, sti, ntpp, n_rows = _tables(tables, M * k)
-    okind = _kind("dout", dout, _FLOAT)
+    okind, H = _kind("dout", dout, _FLOAT), dout.shape[-1]
     ds = _row_stride("dout", dout, dout.dtype, (M, H))
-    _dense("topk_w", topk_w, torch.float32, (M, k))
+    ttp, sti = tables["token_to_perm"], tables["sorted_token_ids"]
+    total, n_rows = tables["num_tokens_post_padded"], _num_rows(tables)
+    t_at, s_at = _table("token_to_perm", ttp, M * k), _table("sorted_token_ids", sti, n_rows)
+    n_at, e_at = _table("num_tokens_post_padded", total, 1), _err(err_word)
+    w_at = _at("topk_w", topk_w, torch.float32, (M, k))
+    r_at = None
     if rows is not None:
         rtype = rows.dtype
-        _dense("rows", rows, rtype, (n_rows, H))
+        r_at = _at("rows", rows, rtype, (n_rows, H))
     elif want_dtopk_w:
         raise ValueError("rows: needed for dtopk_w")
     else:
         rtype = rows_dtype or (drows.dtype if drows is not None else dout.dtype)
     if not want_drows and not want_dtopk_w:
         raise ValueError("neither drows nor dtopk_w is wanted")
-    if rtype not in _FLOAT:
+    rkind = _FLOAT.get(rtype)
+    if rkind is None:
         raise ValueError(f"rows: unsupported type {rtype}")
-    _err(err_word)
-    _on_device(dout, rows, topk_w, ttp, sti, ntpp, drows, dtopk_w, err_word)
     if not want_drows:
         drows = None
-    else:
-        if drows is None:
-            drows = _empty((n_rows, H), rtype, dout.device, stream)
-        _dense("drows", drows, rtype, (n_rows, H))
     if not want_dtopk_w:
         dtopk_w = None
-    else:
-        if dtopk_w is None:
-            dtopk_w = _empty((M, k), torch.float32, dout.device, stream)
-        _dense("dtopk_w", dtopk_w, torch.float32, (M, k))
+    dr_at = None if drows is None else _at("drows", drows, rtype, (n_rows, H))
+    dw_at = None if dtopk_w is None else _at("dtopk_w", dtopk_w, torch.float32, (M, k))
+    dev = _on_device(dout, rows, topk_w, ttp, sti, total, drows, dtopk_w, err_word)
+    if want_drows and dr_at is None:
+        drows = _empty((n_rows, H), rtype, dev, stream)
+        dr_at = drows.data_ptr()
+    if want_dtopk_w and dw_at is None:
+        dtopk_w = _empty((M, k), torch.float32, dev, stream)
+        dw_at = dtopk_w.data_ptr()
     _check("moe_combine_backward", load().moe_combine_backward(
-        _ptr(dout), ds, okind, _ptr(rows), _FLOAT[rtype], _ptr(topk_w), _ptr(ttp), _ptr(sti),
-        _ptr(ntpp), M, k, H, n_rows, _ptr(drows), _ptr(dtopk_w), _ptr(err_word),
-        _stream(stream)))
+        dout.data_ptr(), ds, okind, r_at, rkind, w_at, t_at, s_at, n_at, M, k, H, n_rows, dr_at,
+        dw_at, e_at, _handle(stream, dev)))
     return drows, dtopk_w
 
 
@@ -666,39 +696,40 @@ def moe_topk_softmax_backward(topk_ids: torch.Tensor, topk_w: torch.Tensor,
                               stream=None) -> torch.Tensor:
     """Gradient of moe_topk_softmax: dlogits fp32 [M, E] from the weights'
     gradients dtopk_w [M, k]; 0 for every logit that was not selected."""
-    M, k = topk_w.shape
-    _dense("topk_ids", topk_ids, torch.int32, (M, k))
-    _dense("topk_w", topk_w, torch.float32, (M, k))
-    _dense("dtopk_w", dtopk_w, torch.float32, (M, k))
-    _err(err_word)
-    _on_device(topk_ids, topk_w, dtopk_w, dlogits, err_word)
-    if dlogits is None:
-        dlogits = _empty((M, num_experts), torch.float32, topk_w.device, stream)
-    _dense("dlogits", dlogits, torch.float32, (M, num_experts))
+    M, k = shape = topk_w.shape
+    i_at = _at("topk_ids", topk_ids, torch.int32, shape)
+    w_at = _at("topk_w", topk_w, torch.float32, shape)
+    d_at = _at("dtopk_w", dtopk_w, torch.float32, shape)
+    l_at = None if dlogits is None else _at("dlogits", dlogits, torch.float32, (M, num_experts))
+    e_at = _err(err_word)
+    dev = _on_device(topk_ids, topk_w, dtopk_w, dlogits, err_word)
+    if l_at is None:
+        dlogits = _empty((M, num_experts), torch.float32, dev, stream)
+        l_at = dlogits.data_ptr()
     _check("moe_topk_softmax_backward", load().moe_topk_softmax_backward(
-        _ptr(topk_ids), _ptr(topk_w), _ptr(dtopk_w), M, num_experts, k, _ptr(dlogits),
-        _ptr(err_word), _stream(stream)))
+        i_at, w_at, d_at, M, num_experts, k, l_at, e_at, _handle(stream, dev)))
     return dlogits
+
+
+def _norm_output(name: str, dtype: torch.dtype, M: int, H: int) -> tuple:
+    """(shape, type) of an output of moe_add_rmsnorm on rows of ``dtype``."""
+    if name == "out" or name == "sum":
+        return (M, H), dtype
+    if name == "codes":
+        return (M, H), torch.float8_e4m3fn
+    if name == "scale":
+        return (M, -(-H // 128)), torch.float32
+    if name == "rstd":
+        return (M,), torch.float32
+    raise ValueError(f"no output {name!r}: want out, sum, codes, scale or rstd")
 
 
 def alloc_add_rmsnorm_outputs(x: torch.Tensor, want: Sequence[str], stream=None) -> dict:
     """Buffers for moe_add_rmsnorm: "out", "sum" [M, H] of x's type, "codes"
     float8_e4m3fn [M, H] and "scale" fp32 [M, ceil(H / 128)], "rstd" fp32 [M]."""
     M, H = x.shape
-    made = {}
-    for name in want:
-        if name in ("out", "sum"):
-            shape, dtype = (M, H), x.dtype
-        elif name == "codes":
-            shape, dtype = (M, H), torch.float8_e4m3fn
-        elif name == "scale":
-            shape, dtype = (M, -(-H // 128)), torch.float32
-        elif name == "rstd":
-            shape, dtype = (M,), torch.float32
-        else:
-            raise ValueError(f"want: no output {name!r}")
-        made[name] = _empty(shape, dtype, x.device, stream)
-    return made
+    dev = _on_device(x)
+    return {name: _empty(*_norm_output(name, x.dtype, M, H), dev, stream) for name in want}
 
 
 def moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -709,29 +740,28 @@ def moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     E4M3 with a scale per 128 columns.  Writes the buffers of ``out``, or new
     ones for the outputs in ``want``, and returns them by name."""
     M, H = x.shape
-    kind, wkind = _kind("x", x, _FLOAT), _kind("weight", weight, _FLOAT)
-    xs = _row_stride("x", x, x.dtype, (M, H))
-    rs = 0 if residual is None else _row_stride("residual", residual, x.dtype, (M, H))
-    _dense("weight", weight, weight.dtype, (H,))
-    _on_device(x, weight, residual)
-    if out is None:
-        out = alloc_add_rmsnorm_outputs(x, want, stream)
+    dtype, kind, wkind = x.dtype, _kind("x", x, _FLOAT), _kind("weight", weight, _FLOAT)
+    xs = _row_stride("x", x, dtype, (M, H))
+    rs, r_at = 0, None
+    if residual is not None:
+        rs, r_at = _row_stride("residual", residual, dtype, (M, H)), residual.data_ptr()
+    w_at = _at("weight", weight, weight.dtype, (H,))
+    if out is not None:
+        at = {}
+        for name, t in out.items():
+            shape, otype = _norm_output(name, dtype, M, H)
+            if name == "codes" and t.dtype is torch.uint8:
+                otype = torch.uint8
+            at[name] = _at(name, t, otype, shape)
+        dev = _on_device(x, weight, residual, *out.values())
     else:
-        _on_device(*out.values())
-    shapes = {"out": (M, H), "sum": (M, H), "codes": (M, H), "scale": (M, -(-H // 128)),
-              "rstd": (M,)}
-    for name, t in out.items():
-        if name not in shapes:
-            raise ValueError(f"out: no output {name!r}")
-        if name == "codes":
-            dtype = torch.uint8 if t.dtype == torch.uint8 else torch.float8_e4m3fn
-        else:
-            dtype = torch.float32 if name in ("scale", "rstd") else x.dtype
-        _dense(name, t, dtype, shapes[name])
-    g = out.get
+        dev = _on_device(x, weight, residual)
+        out = {name: _empty(*_norm_output(name, dtype, M, H), dev, stream) for name in want}
+        at = {name: t.data_ptr() for name, t in out.items()}
+    get = at.get
     _check("moe_add_rmsnorm", load().moe_add_rmsnorm(
-        _ptr(x), xs, _ptr(residual), rs, _ptr(weight), kind, wkind, M, H, eps, _ptr(g("sum")),
-        _ptr(g("out")), _ptr(g("codes")), _ptr(g("scale")), _ptr(g("rstd")), _stream(stream)))
+        x.data_ptr(), xs, r_at, rs, w_at, kind, wkind, M, H, eps, get("sum"), get("out"),
+        get("codes"), get("scale"), get("rstd"), _handle(stream, dev)))
     return out
 
 
@@ -751,34 +781,39 @@ def moe_add_rmsnorm_backward(dout: torch.Tensor, sum: torch.Tensor, weight: torc
     dout's type, dweight fp32 [H] or None).  dx is the gradient of x and of
     residual; dsum is the gradient that reaches "sum" from elsewhere.  The
     weight gradient needs a workspace (a new one when None)."""
-    M, H = dout.shape
-    kind, wkind = _kind("dout", dout, _FLOAT), _kind("weight", weight, _FLOAT)
-    ds = _row_stride("dout", dout, dout.dtype, (M, H))
-    ss = _row_stride("sum", sum, dout.dtype, (M, H))
-    es = 0 if dsum is None else _row_stride("dsum", dsum, dout.dtype, (M, H))
-    _dense("weight", weight, weight.dtype, (H,))
-    _dense("rstd", rstd, torch.float32, (M,))
-    _on_device(dout, sum, weight, rstd, dsum, dx, dweight, workspace)
-    if dx is None:
-        dx = _empty((M, H), dout.dtype, dout.device, stream)
-    _dense("dx", dx, dout.dtype, (M, H))
-    nbytes = 0
+    M, H = shape = dout.shape
+    dtype, kind, wkind = dout.dtype, _kind("dout", dout, _FLOAT), _kind("weight", weight, _FLOAT)
+    ds = _row_stride("dout", dout, dtype, shape)
+    ss = _row_stride("sum", sum, dtype, shape)
+    es, d_at = 0, None
+    if dsum is not None:
+        es, d_at = _row_stride("dsum", dsum, dtype, shape), dsum.data_ptr()
+    w_at, r_at = _at("weight", weight, weight.dtype, (H,)), _at("rstd", rstd, torch.float32, (M,))
+    x_at = None if dx is None else _at("dx", dx, dtype, shape)
+    nbytes, g_at, ws_at = 0, None, None
     if not want_dweight:
         dweight = workspace = None
     else:
-        if dweight is None:
-            dweight = _empty((H,), torch.float32, dout.device, stream)
-        _dense("dweight", dweight, torch.float32, (H,))
-        if workspace is None:
-            nbytes = add_rmsnorm_backward_workspace_bytes(M, H)
-            workspace = _empty((nbytes,), torch.uint8, dout.device, stream)
-        else:
+        if dweight is not None:
+            g_at = _at("dweight", dweight, torch.float32, (H,))
+        if workspace is not None:
             if not workspace.is_contiguous():
                 raise ValueError("workspace: want a contiguous tensor")
-            nbytes = workspace.numel() * workspace.element_size()
+            ws_at, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    dev = _on_device(dout, sum, weight, rstd, dsum, dx, dweight, workspace)
+    if x_at is None:
+        dx = _empty((M, H), dtype, dev, stream)
+        x_at = dx.data_ptr()
+    if want_dweight and g_at is None:
+        dweight = _empty((H,), torch.float32, dev, stream)
+        g_at = dweight.data_ptr()
+    if want_dweight and workspace is None:
+        nbytes = add_rmsnorm_backward_workspace_bytes(M, H)
+        workspace = _empty((nbytes,), torch.uint8, dev, stream)
+        ws_at = workspace.data_ptr()
     _check("moe_add_rmsnorm_backward", load().moe_add_rmsnorm_backward(
-        _ptr(dout), ds, _ptr(sum), ss, _ptr(weight), _ptr(rstd), _ptr(dsum), es, kind, wkind, M,
-        H, _ptr(dx), _ptr(dweight), _ptr(workspace), nbytes, _stream(stream)))
+        dout.data_ptr(), ds, sum.data_ptr(), ss, w_at, r_at, d_at, es, kind, wkind, M, H, x_at,
+        g_at, ws_at, nbytes, _handle(stream, dev)))
     return dx, dweight
 
 
@@ -790,23 +825,23 @@ def moe_decode_block(layer: LayerDesc, x: torch.Tensor, residual: Optional[torch
     """The expert half of a block: sum = x + residual, normed = its RMS norm,
     out = moe_decode_layer(normed) with the layer's router weights.  Returns
     (sum, normed); sum_out may be residual's own buffer."""
-    M, H = x.shape
+    M, H = shape = x.shape
     bf16 = torch.bfloat16
     if H != layer.routed.hidden:
         raise ValueError(f"x: want rows of {layer.routed.hidden}, got {H}")
-    if sum_out is None:
-        sum_out = _empty((M, H), bf16, x.device, stream)
-    if normed is None:
-        normed = _empty((M, H), bf16, x.device, stream)
-    for name, t in (("x", x), ("residual", residual), ("out", out), ("sum_out", sum_out),
-                    ("normed", normed)):
-        if t is not None:
-            _dense(name, t, bf16, (M, H))
-    _dense("norm_weight", norm_weight, bf16, (H,))
-    _err(err_word)
-    _on_device(x, residual, norm_weight, out, workspace, sum_out, normed, err_word)
+    x_at, o_at = _at("x", x, bf16, shape), _at("out", out, bf16, shape)
+    r_at = None if residual is None else _at("residual", residual, bf16, shape)
+    s_at = None if sum_out is None else _at("sum_out", sum_out, bf16, shape)
+    n_at = None if normed is None else _at("normed", normed, bf16, shape)
+    w_at, e_at = _at("norm_weight", norm_weight, bf16, (H,)), _err(err_word)
+    dev = _on_device(x, residual, norm_weight, out, workspace, sum_out, normed, err_word)
+    if s_at is None:
+        sum_out = _empty((M, H), bf16, dev, stream)
+        s_at = sum_out.data_ptr()
+    if n_at is None:
+        normed = _empty((M, H), bf16, dev, stream)
+        n_at = normed.data_ptr()
     _check("moe_decode_block", load().moe_decode_block(
-        ctypes.pointer(layer._struct), _ptr(x), _ptr(residual), _ptr(norm_weight), eps, M,
-        _ptr(sum_out), _ptr(normed), _ptr(out), _ptr(workspace), workspace.numel(),
-        _ptr(err_word), _stream(stream)))
+        ctypes.pointer(layer._struct), x_at, r_at, w_at, eps, M, s_at, n_at, o_at,
+        workspace.data_ptr(), workspace.numel(), e_at, _handle(stream, dev)))
     return sum_out, normed

@@ -3,11 +3,13 @@
 // ("fp8_moe_grouped.rs": moe_fp8_grouped_sort's sorted order, which its
 // grouped launchers read through, and moe_weighted_sum_blend_fp8_grouped).
 //
-// All four are token-major: one CTA owns a token, reads the token's row once
-// and touches its top_k sorted rows.  A position-major gather would read
-// every token row top_k times, from HBM once x is larger than the L2.
-// Everything is a copy or a short sum, so HBM bandwidth bounds all of it
+// All four are token-major: a CTA has one token or a few, reads each token's
+// row once and touches its top_k sorted rows.  A position-major gather
+// would read every token row top_k times, from HBM once x is larger than the
+// L2.  Everything is a copy or a short sum, so HBM bandwidth bounds all of it
 // (launch latency at decode sizes).
+#include <type_traits>
+
 #include "common.cuh"
 #include "rows.cuh"
 
@@ -15,7 +17,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxK = 32;        // top_k admitted, as moe_topk_softmax
-constexpr int kPadRows = 8;      // positions whose padding one CTA looks after
+constexpr int kPadRows = 8;      // positions that are looked through for padding together
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
 struct SlotArgs {
@@ -26,69 +28,103 @@ struct SlotArgs {
   uint32_t *err;
 };
 
-// The token's slot positions into shared memory (-1: skipped, or outside the
-// rows, which is reported); threads [0, k) of the CTA.
-__device__ __forceinline__ void load_positions(const SlotArgs &a, int t, int *pos) {
-  if (threadIdx.x < a.k) {
-    int p = __ldcg(a.ttp + (size_t)t * a.k + threadIdx.x);
-    if (p < -1 || p >= a.num_rows) {
-      if (a.err) atomicOr(a.err, MOE_ERR_BAD_POSITION);
-      p = -1;
-    }
-    pos[threadIdx.x] = p;
+// The sorted position of a slot; -1: skipped, or outside the rows, which is
+// reported.
+__device__ __forceinline__ int position(const SlotArgs &a, size_t slot) {
+  int p = __ldcg(a.ttp + slot);
+  if (p < -1 || p >= a.num_rows) {
+    if (a.err) atomicOr(a.err, MOE_ERR_BAD_POSITION);
+    p = -1;
   }
+  return p;
 }
 
-// Of the kPadRows positions of this CTA, the bits of those that hold padding:
-// positions below the total whose slot is none.  Called by whole warps; every
-// warp gets the same bits.
-__device__ __forceinline__ unsigned padding_mask(const SlotArgs &a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t p = (int64_t)blockIdx.x * kPadRows + lane;
-  bool pad = false;
-  if (lane < kPadRows && p < a.num_rows) {
-    const int s = __ldcg(a.sti + p);
-    pad = p < __ldcg(a.total) && (s < 0 || s >= a.M * a.k);
+// The padding rows (positions below the total whose slot is none) of a CTA's
+// share: groups of eight positions, dealt to the CTAs in turn, since an
+// expert's padding is one run and would be one CTA's otherwise.  look() reads
+// four groups' slots, early in the kernel, so that their latency passes with
+// the tokens' own; clear() calls f(p) for each padding row, the whole CTA at
+// it.  Whole warps; every warp sees the same.
+struct Padding {
+  int64_t group;
+  int total, slot;   // rows in use; the slot at this lane's position
+
+  __device__ __forceinline__ int64_t at() const {
+    const int lane = threadIdx.x & 31;
+    return (group + (lane >> 3) * (int64_t)gridDim.x) * kPadRows + (lane & 7);
   }
-  return __ballot_sync(kFull, pad);
-}
+  __device__ __forceinline__ void look(const SlotArgs &a) {
+    group = blockIdx.x;
+    total = 0;
+    if (a.num_rows > 0) total = __ldcg(a.total);
+    if (at() < a.num_rows) slot = __ldcg(a.sti + at());
+  }
+  template <typename F>
+  __device__ __forceinline__ void clear(const SlotArgs &a, F &&f) {
+    const int64_t stride = gridDim.x;
+    total = min(total, a.num_rows);
+    while (group * kPadRows < total) {
+      const bool pad = at() < total && (slot < 0 || slot >= a.M * a.k);
+      for (unsigned m = __ballot_sync(kFull, pad); m; m &= m - 1) {
+        const int b = __ffs(m) - 1;
+        f((group + (b >> 3) * stride) * kPadRows + (b & 7));
+      }
+      group += 4 * stride;
+      if (at() < total) slot = __ldcg(a.sti + at());
+    }
+  }
+};
 
 // ---------------------------------------------------------------------------
 // dispatch: rows[token_to_perm[t][j]] = x[t]
 // ---------------------------------------------------------------------------
 //
-// A copy of bytes in units U (16-byte where the rows allow it), so one kernel
-// serves every type.
+// A copy of bytes, so one kernel serves every type (ES: the element's bytes,
+// for rows that are moved element by element).  A CTA takes TOK tokens and, in
+// grid.y, a part of the row, one 16-byte piece a thread.  Bound by the writes.
 
-template <typename U>
-__global__ void __launch_bounds__(256) dispatch_kernel(SlotArgs a, const U *x, int64_t x_stride,
-                                                       const float *xs, int units, int scales,
-                                                       U *rows, float *rs) {
-  __shared__ int pos[kMaxK];
+template <int ES, int TOK, int A>
+__global__ void __launch_bounds__(256) dispatch_kernel(SlotArgs a, const char *x, int64_t x_stride,
+                                                       const float *xs, int len, int scales,
+                                                       char *rows, float *rs) {
+  __shared__ int pos[kMaxK];   // TOK * k <= kMaxK
   pdl_wait();
   pdl_trigger();
-  const int t = blockIdx.x, nt = blockDim.x;
-  const unsigned pads = padding_mask(a);
-  if (t < a.M) {
-    load_positions(a, t, pos);
-    const U *src = x + t * x_stride;
+  const int tid = threadIdx.x, at = (blockIdx.y * blockDim.x + tid) * 16;
+  const bool on = at < len;
+  const int64_t t0 = (int64_t)blockIdx.x * TOK;
+  auto put = [&](int64_t p, const uint4 &v) { store16<ES, A>(rows + p * len, at, len, v, on); };
+  Padding padding;
+  padding.look(a);
+  if (t0 < a.M) {
+    uint4 v[TOK];
+#pragma unroll
+    for (int i = 0; i < TOK; ++i) {
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (on && t0 + i < a.M) v[i] = load16<ES, A>(x + (t0 + i) * x_stride, at, len);
+    }
+    const int n = (int)min((int64_t)TOK, a.M - t0) * a.k;
+    if (tid < n) pos[tid] = position(a, t0 * a.k + tid);
     __syncthreads();
-    for (int c = threadIdx.x; c < units; c += nt) {
-      const U v = __ldg(src + c);
+#pragma unroll
+    for (int i = 0; i < TOK; ++i) {
+      if (t0 + i >= a.M) break;
       for (int j = 0; j < a.k; ++j)
-        if (pos[j] >= 0) rows[(size_t)pos[j] * units + c] = v;
+        if (const int p = pos[i * a.k + j]; p >= 0) put(p, v[i]);
     }
-    for (int c = threadIdx.x; c < scales; c += nt) {
-      const float v = __ldg(xs + (size_t)t * scales + c);
-      for (int j = 0; j < a.k; ++j)
-        if (pos[j] >= 0) rs[(size_t)pos[j] * scales + c] = v;
-    }
+    if (blockIdx.y == 0)
+      for (int i = tid; i < n / a.k * scales; i += blockDim.x) {
+        const int t = i / scales, col = i - t * scales;
+        const float q = __ldg(xs + (t0 + t) * scales + col);
+        for (int j = 0; j < a.k; ++j)
+          if (pos[t * a.k + j] >= 0) rs[(size_t)pos[t * a.k + j] * scales + col] = q;
+      }
   }
-  for (unsigned m = pads; m; m &= m - 1) {
-    const size_t p = (size_t)blockIdx.x * kPadRows + (__ffs(m) - 1);
-    for (int c = threadIdx.x; c < units; c += nt) rows[p * units + c] = U{};
-    for (int c = threadIdx.x; c < scales; c += nt) rs[p * scales + c] = 0.f;
-  }
+  padding.clear(a, [&](int64_t p) {
+    put(p, make_uint4(0, 0, 0, 0));
+    if (blockIdx.y == 0)
+      for (int i = tid; i < scales; i += blockDim.x) rs[(size_t)p * scales + i] = 0.f;
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -96,42 +132,75 @@ __global__ void __launch_bounds__(256) dispatch_kernel(SlotArgs a, const U *x, i
 // ---------------------------------------------------------------------------
 //
 // fp32, j ascending, rounded once.  Without weights it is the gradient of
-// the dispatch.  The loads of U slots' chunks are issued before any is used.
+// the dispatch.  A CTA takes the `slots` of some tokens (at most 32) and, in
+// grid.y, a part of the row, one 16-byte piece a thread.  Its first warp
+// lists the slots that are there; eight loads are issued before any is used,
+// so that as much is in flight with few slots a token, or many skipped, as
+// with top_k = 8.
 
-template <typename R, typename O, bool WEIGHTED, bool VEC>
+constexpr int kBatch = 8;
+
+template <typename R, typename O, bool WEIGHTED, int A>
 __global__ void __launch_bounds__(256) combine_kernel(SlotArgs a, const typename R::bits *rows,
-                                                      const float *w, int H,
+                                                      const float *w, int H, int tok,
                                                       typename O::bits *out) {
-  constexpr int U = sizeof(typename R::bits) == 2 ? 8 : 4;
-  __shared__ int pos[kMaxK];
+  constexpr int N = kPer16<R>;
+  __shared__ int pos[kMaxK];    // of the listed slots; -1: a token without any
   __shared__ float wt[kMaxK];
+  __shared__ int ends[kMaxK];   // the token that a listed slot is the last of, or -1
+  __shared__ int count;
   pdl_wait();
   pdl_trigger();
-  const int t = blockIdx.x;
-  load_positions(a, t, pos);
-  if (WEIGHTED && threadIdx.x < a.k) wt[threadIdx.x] = __ldcg(w + (size_t)t * a.k + threadIdx.x);
+  const int64_t t0 = (int64_t)blockIdx.x * tok;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, t = lane / a.k, j = lane - t * a.k;
+    const bool slot = t < tok && t0 + t < a.M;
+    int p = -1;
+    float wj = 0.f;
+    if (slot) {
+      p = position(a, (t0 + t) * a.k + j);
+      if (WEIGHTED) wj = __ldcg(w + (t0 + t) * a.k + j);
+    }
+    const unsigned there = __ballot_sync(kFull, p >= 0);
+    const unsigned mine = (a.k == 32 ? kFull : ((1u << a.k) - 1) << (t * a.k));   // of the token
+    const unsigned listed =
+        __ballot_sync(kFull, p >= 0 || (slot && j == 0 && (there & mine) == 0));
+    if (listed >> lane & 1) {
+      const int at = __popc(listed & lanemask_lt());
+      pos[at] = p;
+      wt[at] = wj;
+      ends[at] = (listed & mine) >> lane == 1 ? t : -1;
+    }
+    if (lane == 0) count = __popc(listed);
+  }
   __syncthreads();
-  const int chunks = (H + kChunk - 1) / kChunk;
-  for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
-    float acc[kChunk] = {};
-    for (int j0 = 0; j0 < a.k; j0 += U) {
-      Raw<R> v[U];
+  const int c = blockIdx.y * blockDim.x + threadIdx.x;
+  const bool on = c < (H + N - 1) / N;
+  if (A == kWhole && !on) return;   // kElems: whole warps up to the stores
+  const int n = count;
+  f32x2 acc[N / 2] = {};
+  for (int s0 = 0; s0 < n; s0 += kBatch) {
+    Raw<R, N> v[kBatch];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (j0 + u < a.k && pos[j0 + u] >= 0)
-          v[u] = raw_load<R, VEC>(rows + (size_t)pos[j0 + u] * H, c, H);
+    for (int u = 0; u < kBatch; ++u)
+      if ((A == kWhole || on) && s0 + u < n && pos[s0 + u] >= 0)
+        v[u] = raw_load<R, N, A>(rows + (size_t)pos[s0 + u] * H, c, H);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (j0 + u < a.k && pos[j0 + u] >= 0) {
-          float f[kChunk];
-          raw_up<R>(v[u], f);
-          const float wj = WEIGHTED ? wt[j0 + u] : 1.f;
+    for (int u = 0; u < kBatch; ++u) {
+      if (s0 + u >= n) break;
+      if ((A == kWhole || on) && pos[s0 + u] >= 0) {
+        f32x2 f[N / 2];
+        raw_up<R, N>(v[u], f);
+        const float wj = WEIGHTED ? wt[s0 + u] : 1.f;
 #pragma unroll
-          for (int i = 0; i < kChunk; ++i) acc[i] = WEIGHTED ? fmaf(wj, f[i], acc[i]) : acc[i] + f[i];
-        }
+        for (int e = 0; e < N / 2; ++e) acc[e] = fma2(pair(wj, wj), f[e], acc[e]);
+      }
+      if (const int t = ends[s0 + u]; t >= 0) {
+        raw_store<O, N, A>(out + (t0 + t) * H, c, H, raw_down<O>(acc), A == kWhole || on);
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) acc[e] = 0;
       }
     }
-    raw_store<O, VEC>(out + (size_t)t * H, c, H, raw_down<O>(acc));
   }
 }
 
@@ -141,61 +210,78 @@ __global__ void __launch_bounds__(256) combine_kernel(SlotArgs a, const typename
 //
 //   drows[token_to_perm[t][j]] = w[t][j] * dout[t],
 //   dw[t][j] = sum_c dout[t][c] * rows[token_to_perm[t][j]][c]   (fp32).
-// Eight slots at a time: a thread keeps their eight partial dot products,
-// a warp ends them with a reduce-scatter butterfly (16 -> 8 -> 4 lanes hold
-// 4 -> 2 -> 1 sums), the warps' sums are added in warp order.  The order
-// depends on hidden alone: a token's bits are the same in every batch.
+// A CTA takes TOK tokens and U = 8 / TOK slots of each at a time; its threads
+// walk over the row in 16-byte pieces, all eight slots' loads issued before
+// any is used.  A thread keeps the eight partial dot products, a warp ends
+// them with a reduce-scatter butterfly (16 -> 8 -> 4 lanes hold 4 -> 2 -> 1
+// sums), the warps' sums are added in warp order.  A sum's order depends on
+// hidden and the type alone: a token's bits are the same in every batch.
 
-template <typename R, typename O, bool DW, bool DR, bool VEC>
-__global__ void __launch_bounds__(256) combine_grad_kernel(SlotArgs a,
-                                                           const typename O::bits *dout,
-                                                           int64_t dout_stride,
-                                                           const typename R::bits *rows,
-                                                           const float *w, int H,
-                                                           typename R::bits *drows, float *dw) {
-  constexpr int U = 8;
-  __shared__ int pos[kMaxK];
+template <typename R, typename O, int TOK, bool DW, bool DR, int A>
+__global__ void __launch_bounds__(256, DR ? 3 : TOK > 1 ? 3 : 4) combine_grad_kernel(
+    SlotArgs a, const typename O::bits *dout, int64_t dout_stride, const typename R::bits *rows,
+    const float *w, int H, typename R::bits *drows, float *dw) {
+  constexpr int N = kPer16<R>, U = 8 / TOK;
+  __shared__ int pos[kMaxK];   // TOK * k <= kMaxK
   __shared__ float wt[kMaxK];
-  __shared__ float red[8][U];
+  __shared__ float red[8][8];
   pdl_wait();
   pdl_trigger();
-  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nwarps = blockDim.x >> 5;
-  const unsigned pads = DR ? padding_mask(a) : 0u;
-  const int chunks = (H + kChunk - 1) / kChunk;
-  if (t < a.M) {
-    load_positions(a, t, pos);
-    if (DR && tid < a.k) wt[tid] = __ldcg(w + (size_t)t * a.k + tid);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
+  const int pieces = (H + N - 1) / N;
+  const int64_t t0 = (int64_t)blockIdx.x * TOK;
+  Padding padding;
+  if (DR) padding.look(a);
+  if (t0 < a.M) {
+    const int n = (int)min((int64_t)TOK, a.M - t0) * a.k;
+    if (tid < TOK * a.k) {
+      pos[tid] = tid < n ? position(a, t0 * a.k + tid) : -1;
+      if (DR) wt[tid] = tid < n ? __ldcg(w + t0 * a.k + tid) : 0.f;
+    }
     __syncthreads();
-    const typename O::bits *drow = dout + t * dout_stride;
     for (int j0 = 0; j0 < a.k; j0 += U) {
-      float acc[U] = {};
-      for (int c = tid; c < chunks; c += blockDim.x) {
-        const Raw<O> dr = raw_load<O, VEC>(drow, c, H);
-        Raw<R> v[U];
+      float acc[8] = {};   // slot u of token i at i * U + u
+      // kElems: whole warps up to the stores
+      for (int c = tid; (A == kElems ? c - lane : c) < pieces; c += blockDim.x) {
+        const bool on = A != kElems || c < pieces;
+        Raw<O, N> dr[TOK];
+        Raw<R, N> v[TOK][U];
+#pragma unroll
+        for (int i = 0; i < TOK; ++i)
+          dr[i] = on && (TOK == 1 || t0 + i < a.M)
+                      ? raw_load<O, N, A>(dout + (t0 + i) * dout_stride, c, H)
+                      : raw_zero<O, N>();
         if (DW) {
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (j0 + u < a.k && pos[j0 + u] >= 0)
-              v[u] = raw_load<R, VEC>(rows + (size_t)pos[j0 + u] * H, c, H);
-        }
-        float d[kChunk];
-        raw_up<O>(dr, d);
+          for (int i = 0; i < TOK; ++i)
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (j0 + u < a.k && pos[j0 + u] >= 0) {
-            if (DR) {
-              float g[kChunk];
-              const float wj = wt[j0 + u];
-#pragma unroll
-              for (int i = 0; i < kChunk; ++i) g[i] = wj * d[i];
-              raw_store<R, VEC>(drows + (size_t)pos[j0 + u] * H, c, H, raw_down<R>(g));
+            for (int u = 0; u < U; ++u) {
+              const int s = i * a.k + j0 + u;
+              if (on && j0 + u < a.k && pos[s] >= 0)
+                v[i][u] = raw_load<R, N, A>(rows + (size_t)pos[s] * H, c, H);
             }
-            if (DW) {
-              float f[kChunk];
-              raw_up<R>(v[u], f);
+        }
 #pragma unroll
-              for (int i = 0; i < kChunk; ++i) acc[u] = fmaf(d[i], f[i], acc[u]);
+        for (int i = 0; i < TOK; ++i) {
+          float d[N];
+          raw_up<O, N>(dr[i], d);
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int s = i * a.k + j0 + u;
+            if (j0 + u < a.k && pos[s] >= 0) {
+              if (DR) {
+                float g[N];
+                const float wj = wt[s];
+#pragma unroll
+                for (int e = 0; e < N; ++e) g[e] = wj * d[e];
+                raw_store<R, N, A>(drows + (size_t)pos[s] * H, c, H, raw_down<R, N>(g), on);
+              }
+              if (DW && on) {
+                float f[N];
+                raw_up<R, N>(v[i][u], f);
+#pragma unroll
+                for (int e = 0; e < N; ++e) acc[i * U + u] = fmaf(d[e], f[e], acc[i * U + u]);
+              }
             }
           }
         }
@@ -216,72 +302,108 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(SlotArgs a,
         s1 += __shfl_xor_sync(kFull, s1, 1);
         if ((lane & 3) == 0) red[warp][lane >> 2] = s1;
         __syncthreads();
-        if (tid < U && j0 + tid < a.k) {
-          float v = red[0][tid];
-          for (int i = 1; i < nwarps; ++i) v += red[i][tid];
-          dw[(size_t)t * a.k + j0 + tid] = pos[j0 + tid] >= 0 ? v : 0.f;
+        if (tid < 8) {
+          const int i = tid / U, j = j0 + tid % U;
+          if (t0 + i < a.M && j < a.k) {
+            float v = red[0][tid];
+            for (int x = 1; x < nwarps; ++x) v += red[x][tid];
+            dw[(t0 + i) * a.k + j] = pos[i * a.k + j] >= 0 ? v : 0.f;
+          }
         }
         if (j0 + U < a.k) __syncthreads();   // red is written again
       }
     }
   }
-  if (DR) {
-    for (unsigned m = pads; m; m &= m - 1) {
-      const size_t p = (size_t)blockIdx.x * kPadRows + (__ffs(m) - 1);
-      for (int c = tid; c < chunks; c += blockDim.x)
-        raw_store<R, VEC>(drows + p * H, c, H, raw_zero<R>());
-    }
-  }
+  if (DR)
+    padding.clear(a, [&](int64_t p) {
+      for (int c = tid; c - lane < pieces; c += blockDim.x)
+        raw_store<R, N, A>(drows + p * H, c, H, raw_zero<R, N>(), c < pieces);
+    });
 }
 
-// Threads of a CTA: one chunk of eight elements each, up to 256.
-dim3 row_threads(int pieces) {
-  const int t = (pieces + 31) / 32 * 32;
-  return dim3(t > 256 ? 256 : t);
+// The row in equal parts of at most 256 pieces, one a thread.
+struct Parts {
+  int parts, threads;
+};
+Parts split_parts(int pieces) {
+  const int parts = (pieces + 255) / 256;
+  return Parts{parts, ((pieces + parts - 1) / parts + 31) / 32 * 32};
 }
 
-// CTAs of a kernel that also clears padding rows: one per token, and as many
-// as look after every position.
-dim3 token_grid(int M, int num_rows) {
-  const int pads = (int)ceil_div64(num_rows, kPadRows);
-  return dim3(M > pads ? M : pads);
+// CTAs of a kernel that clears padding besides its tokens: with few tokens, up
+// to one for every eight positions.
+int64_t pad_ctas(int64_t ctas, int num_rows) {
+  const int64_t pads = ceil_div64(num_rows, kPadRows);
+  const int64_t most = 8 * (int64_t)sm_count();
+  return pads <= ctas || ctas >= most ? ctas : pads < most ? pads : most;
 }
 
-template <typename R, typename O>
-int launch_combine(const SlotArgs &a, const void *rows, const float *w, int H, void *out, bool vec,
+template <typename R, typename O, bool WEIGHTED>
+int launch_combine(const SlotArgs &a, const void *rows, const float *w, int H, void *out, int align,
                    void *stream) {
-  const dim3 grid(a.M), block = row_threads((H + kChunk - 1) / kChunk);
+  const Parts s = split_parts((H + kPer16<R> - 1) / kPer16<R>);
+  // Up to eight tokens and 32 slots a CTA while eight CTAs an SM remain: at
+  // M = 4000, top_k = 6, hidden = 2880 with three of four slots skipped 23.4 us
+  // with one token a CTA and 13.9 with five; at top_k = 8 with none skipped
+  // (M = 4096, hidden = 7168) 98.7 and 85.3.
+  const int64_t room = (int64_t)a.M * s.parts / (8 * sm_count());
+  const int fit = 32 / a.k < 8 ? 32 / a.k : 8;
+  const int tok = room < 1 ? 1 : room < fit ? (int)room : fit;
+  const dim3 grid((unsigned)ceil_div64(a.M, tok), s.parts), block(s.threads);
   auto r = static_cast<const typename R::bits *>(rows);
   auto o = static_cast<typename O::bits *>(out);
-  if (w)
-    return vec ? launch_pdl(combine_kernel<R, O, true, true>, grid, block, 0, stream, a, r, w, H, o)
-               : launch_pdl(combine_kernel<R, O, true, false>, grid, block, 0, stream, a, r, w, H, o);
-  return vec ? launch_pdl(combine_kernel<R, O, false, true>, grid, block, 0, stream, a, r, w, H, o)
-             : launch_pdl(combine_kernel<R, O, false, false>, grid, block, 0, stream, a, r, w, H, o);
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, grid, block, 0, stream, a, r, w, H, tok, o);
+  };
+  return by_align<!std::is_same_v<R, O>>(align, [&](auto al) {
+    return go(combine_kernel<R, O, WEIGHTED, decltype(al)::value>);
+  });
+}
+
+template <typename R, typename O, int TOK, bool DW, bool DR>
+int launch_combine_grad(const SlotArgs &a, const void *dout, int64_t stride, const void *rows,
+                        const float *w, int H, void *drows, float *dw, int align, void *stream) {
+  const int pieces = (H + kPer16<R> - 1) / kPer16<R>;
+  const int threads = pieces >= 256 ? 256 : (pieces + 31) / 32 * 32;
+  int64_t ctas = ceil_div64(a.M, TOK);
+  if (DR) ctas = pad_ctas(ctas, a.num_rows);
+  const dim3 grid((unsigned)ctas), block(threads);
+  auto d = static_cast<const typename O::bits *>(dout);
+  auto r = static_cast<const typename R::bits *>(rows);
+  auto g = static_cast<typename R::bits *>(drows);
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, grid, block, 0, stream, a, d, stride, r, w, H, g, dw);
+  };
+  return by_align<!std::is_same_v<R, O>>(align, [&](auto al) {
+    return go(combine_grad_kernel<R, O, TOK, DW, DR, decltype(al)::value>);
+  });
 }
 
 template <typename R, typename O, bool DW, bool DR>
 int launch_combine_grad(const SlotArgs &a, const void *dout, int64_t stride, const void *rows,
-                        const float *w, int H, void *drows, float *dw, bool vec, void *stream) {
-  const dim3 grid = DR ? token_grid(a.M, a.num_rows) : dim3(a.M);
-  const dim3 block = row_threads((H + kChunk - 1) / kChunk);
-  auto d = static_cast<const typename O::bits *>(dout);
-  auto r = static_cast<const typename R::bits *>(rows);
-  auto g = static_cast<typename R::bits *>(drows);
-  return vec ? launch_pdl(combine_grad_kernel<R, O, DW, DR, true>, grid, block, 0, stream, a, d,
-                          stride, r, w, H, g, dw)
-             : launch_pdl(combine_grad_kernel<R, O, DW, DR, false>, grid, block, 0, stream, a, d,
-                          stride, r, w, H, g, dw);
+                        const float *w, int H, void *drows, float *dw, int align, void *stream) {
+  // Eight slots a CTA in flight when there are tokens enough: at M = 16384,
+  // top_k = 1, hidden = 1024 44.6 us with one token a CTA and 22.3 with four.
+  const int tok = a.M < 1024 || a.k > 4 ? 1 : a.k > 2 ? 2 : 4;
+  auto go = [&](auto t) {
+    return launch_combine_grad<R, O, decltype(t)::value, DW, DR>(a, dout, stride, rows, w, H, drows,
+                                                                 dw, align, stream);
+  };
+  if (tok == 4) return go(std::integral_constant<int, 4>{});
+  if (tok == 2) return go(std::integral_constant<int, 2>{});
+  return go(std::integral_constant<int, 1>{});
 }
 
 template <typename R, typename O>
 int launch_combine_grad(const SlotArgs &a, const void *dout, int64_t stride, const void *rows,
-                        const float *w, int H, void *drows, float *dw, bool vec, void *stream) {
-  if (drows && dw)
-    return launch_combine_grad<R, O, true, true>(a, dout, stride, rows, w, H, drows, dw, vec, stream);
-  if (dw)
-    return launch_combine_grad<R, O, true, false>(a, dout, stride, rows, w, H, drows, dw, vec, stream);
-  return launch_combine_grad<R, O, false, true>(a, dout, stride, rows, w, H, drows, dw, vec, stream);
+                        const float *w, int H, void *drows, float *dw, int align, void *stream) {
+  auto go = [&](auto d, auto r) {
+    return launch_combine_grad<R, O, decltype(d)::value, decltype(r)::value>(
+        a, dout, stride, rows, w, H, drows, dw, align, stream);
+  };
+  if (drows && dw) return go(std::true_type{}, std::true_type{});
+  if (dw) return go(std::true_type{}, std::false_type{});
+  return go(std::false_type{}, std::true_type{});
 }
 
 // Host checks shared by the four entry points; MOE_OK with *a filled.
@@ -289,7 +411,8 @@ int slot_args(SlotArgs *a, int M, int top_k, int hidden, int num_rows,
               const int32_t *token_to_perm, const int32_t *sorted_token_ids,
               const int32_t *num_tokens_post_padded, uint32_t *err_word) {
   if (M < 0 || top_k < 1 || hidden < 1 || num_rows < 0) return MOE_EINVAL;
-  if (top_k > kMaxK || (int64_t)M * top_k > MOE_MAX_SLOTS) return MOE_EUNSUPPORTED;
+  if (hidden > MOE_MAX_ROW_HIDDEN || top_k > kMaxK || (int64_t)M * top_k > MOE_MAX_SLOTS)
+    return MOE_EUNSUPPORTED;
   if (M > 0 && !token_to_perm) return MOE_EINVAL;
   *a = SlotArgs{token_to_perm, sorted_token_ids, num_tokens_post_padded, M, top_k, num_rows,
                 err_word};
@@ -307,6 +430,13 @@ int with_types(int rows_dtype, int out_dtype, F &&f) {
   return MOE_EUNSUPPORTED;
 }
 
+// The alignment of a call from its expert rows' and its token rows' own: of a
+// mixed pair, 16 bytes of fp32 meet 8 of the 16-bit type, whole or by elements.
+int pair_alignment(int rows, int tokens, int rb, int ob) {
+  if (rb == ob) return rows < tokens ? rows : tokens;
+  return rows == 16 && tokens >= 8 ? kWhole : kElems;
+}
+
 bool float_dtype(int d) {
   return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F16 || d == MOE_DTYPE_F32;
 }
@@ -322,11 +452,16 @@ int combine(const void *rows, int rows_dtype, const float *topk_w, const int32_t
   const int rb = dtype_bytes(rows_dtype), ob = dtype_bytes(out_dtype);
   if ((M > 0 && !out) || (num_rows > 0 && !rows)) return MOE_EINVAL;
   if (!elem_aligned(rows, rb) || !elem_aligned(out, ob)) return MOE_EINVAL;
-  const bool vec = hidden % kChunk == 0 && rows_vector(rows, hidden, rb) &&
-                   rows_vector(out, hidden, ob);
+  const int align = pair_alignment(rows_alignment(rows, hidden, hidden, rb),
+                                   rows_alignment(out, hidden, hidden, ob), rb, ob);
   return with_types(rows_dtype, out_dtype, [&](auto R, auto O) {
     if (M == 0) return MOE_OK;
-    return launch_combine<decltype(R), decltype(O)>(a, rows, topk_w, hidden, out, vec, stream);
+    using RT = decltype(R);
+    using OT = decltype(O);
+    // without weights (the gradient of the dispatch) both types are one
+    if constexpr (std::is_same_v<RT, OT>)
+      if (!topk_w) return launch_combine<RT, OT, false>(a, rows, topk_w, hidden, out, align, stream);
+    return launch_combine<RT, OT, true>(a, rows, topk_w, hidden, out, align, stream);
   });
 }
 
@@ -352,25 +487,38 @@ extern "C" int moe_dispatch(const void *x, int64_t x_stride, const float *x_scal
   if (!elem_aligned(x, eb) || !elem_aligned(rows, eb) || !elem_aligned(x_scale, 4) ||
       !elem_aligned(rows_scale, 4))
     return MOE_EINVAL;
-  const dim3 grid = token_grid(M, num_rows);
-  if (grid.x == 0) return MOE_OK;
+  if (M == 0 && num_rows == 0) return MOE_OK;
   const int scales = dtype == MOE_DTYPE_E4M3 ? (hidden + 127) / 128 : 0;
-  // the widest unit that every row's start and length are multiples of
-  const uint64_t bits = (uint64_t)(uintptr_t)x | (uint64_t)(uintptr_t)rows |
-                        (uint64_t)hidden * eb | (uint64_t)x_stride * eb;
-  auto go = [&](auto unit) {
-    using U = decltype(unit);
-    const int64_t per = sizeof(U);
-    const int units = (int)((int64_t)hidden * eb / per);
-    return launch_pdl(dispatch_kernel<U>, grid, row_threads(units), 0, stream, a,
-                      static_cast<const U *>(x), x_stride * eb / per, x_scale, units, scales,
-                      static_cast<U *>(rows), rows_scale);
+  const int len = hidden * eb;
+  int align = rows_alignment(x, x_stride, hidden, eb);
+  if (const int k = rows_alignment(rows, hidden, hidden, eb); k < align) align = k;
+  const Parts s = split_parts((len + 15) / 16);
+  // two tokens a CTA at least when there are many (M = 4000, top_k = 6: 16.0 us
+  // with one, 12.9 with two), more with fewer slots (M = 16384, top_k = 1: 18.5
+  // and, with eight, 13.0)
+  const int most = kMaxK / top_k;
+  int tok = M < 1024 ? 1 : top_k == 1 ? 8 : top_k == 2 ? 4 : 2;
+  if (tok > most) tok = most;
+  const dim3 grid((unsigned)pad_ctas(ceil_div64(M, tok), num_rows), s.parts), block(s.threads);
+  auto launch = [&](auto kernel) {
+    return launch_pdl(kernel, grid, block, 0, stream, a, static_cast<const char *>(x),
+                      x_stride * eb, x_scale, len, scales, static_cast<char *>(rows), rows_scale);
   };
-  if (bits % 16 == 0) return go(uint4{});
-  if (bits % 8 == 0) return go(uint2{});
-  if (bits % 4 == 0) return go(uint32_t{});
-  if (bits % 2 == 0) return go(uint16_t{});
-  return go(uint8_t{});
+  auto go = [&](auto es, auto al) {
+    constexpr int ES = decltype(es)::value, A = decltype(al)::value;
+    if (tok == 8) return launch(dispatch_kernel<ES, 8, A>);
+    if (tok == 4) return launch(dispatch_kernel<ES, 4, A>);
+    if (tok == 2) return launch(dispatch_kernel<ES, 2, A>);
+    return launch(dispatch_kernel<ES, 1, A>);
+  };
+  // by pieces and halves every type is the same
+  return by_align(align, [&](auto al) {
+    if constexpr (decltype(al)::value == kElems) {
+      if (eb == 4) return go(std::integral_constant<int, 4>{}, al);
+      if (eb == 2) return go(std::integral_constant<int, 2>{}, al);
+    }
+    return go(std::integral_constant<int, 1>{}, al);
+  });
 }
 
 extern "C" int moe_dispatch_backward(const void *drows, int dtype, int M, int top_k, int hidden,
@@ -409,11 +557,13 @@ extern "C" int moe_combine_backward(const void *dout, int64_t dout_stride, int o
   if (drows && num_rows > 0 && (!sorted_token_ids || !num_tokens_post_padded)) return MOE_EINVAL;
   if (!elem_aligned(dout, ob) || !elem_aligned(rows, rb) || !elem_aligned(drows, rb))
     return MOE_EINVAL;
-  const bool vec = hidden % kChunk == 0 && rows_vector(dout, dout_stride, ob) &&
-                   rows_vector(rows, hidden, rb) && rows_vector(drows, hidden, rb);
+  const int ar = rows_alignment(rows, hidden, hidden, rb);
+  const int ag = rows_alignment(drows, hidden, hidden, rb);
+  const int align = pair_alignment(ar < ag ? ar : ag,
+                                   rows_alignment(dout, dout_stride, hidden, ob), rb, ob);
   return with_types(rows_dtype, out_dtype, [&](auto R, auto O) {
     if (M == 0 && (!drows || num_rows == 0)) return MOE_OK;
     return launch_combine_grad<decltype(R), decltype(O)>(a, dout, dout_stride, rows, topk_w,
-                                                         hidden, drows, dtopk_w, vec, stream);
+                                                         hidden, drows, dtopk_w, align, stream);
   });
 }

@@ -3,6 +3,7 @@
 // (moe_add_rmsnorm_backward).
 #include <math.h>
 
+
 #include "common.cuh"
 #include "rows.cuh"
 
@@ -10,14 +11,18 @@ namespace moe {
 namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr int kMaxWarps = 16;         // warps of a CTA
 constexpr float kE4m3Max = 448.f;
 constexpr float kScaleMin = 1.17549435e-38f;   // 2^-126, the smallest normal
 
-// max that keeps a NaN.
+// Maxima that keep a NaN: of two, and of three magnitudes.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -29,146 +34,300 @@ __device__ __forceinline__ uint16_t to_e4m3x2(float lo, float hi) {
 }
 
 // Sum over the threads of a row group (blockDim.x threads, whole warps):
-// butterfly in the warp, then the warps in order.  `red` has kMaxWarps floats
-// per call in flight; one barrier.
+// butterfly in the warp, then the warps' sums four by four.  One barrier, of
+// the group alone; calls that follow one another take turns between two
+// `red`s, whose unused places are zero.
+constexpr int kRedFloats = 64;   // a multiple of four per group, 48 at most (12 groups of two warps)
 __device__ __forceinline__ float group_sum(float v, float *red) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
   const int nw = blockDim.x >> 5;
   if (nw == 1) return v;
-  const int base = threadIdx.y * nw;
-  if ((threadIdx.x & 31) == 0) red[base + (threadIdx.x >> 5)] = v;
-  __syncthreads();
-  v = red[base];
-  for (int i = 1; i < nw; ++i) v += red[base + i];
+  float *mine = red + threadIdx.y * ((nw + 3) & ~3);
+  if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.y), "r"(blockDim.x) : "memory");
+  v = 0.f;
+  for (int i = 0; i < nw; i += 4) {
+    const float4 q = *reinterpret_cast<const float4 *>(mine + i);
+    v += (q.x + q.y) + (q.z + q.w);
+  }
   return v;
 }
-
-// How a row of H elements is split: TPR threads (whole warps) of CH chunks
-// each, thread i taking the chunks i, i + TPR, ...; a function of H alone, so
-// that a row's bits do not depend on the batch.  Narrow rows share a CTA.
-struct Split {
-  int ch, tpr, rows;
-};
-Split split_row(int H, int cta_threads) {
-  const int chunks = (H + kChunk - 1) / kChunk;
-  const int ch = chunks <= 256 ? 1 : chunks <= 512 ? 2 : 4;
-  const int tpr = ((chunks + ch - 1) / ch + 31) / 32 * 32;
-  return Split{ch, tpr, tpr >= cta_threads ? 1 : cta_threads / tpr};
+// Before the first group_sum; the whole CTA.
+__device__ __forceinline__ void clear_red(float (&red)[2][kRedFloats]) {
+  const int i = threadIdx.y * blockDim.x + threadIdx.x;
+  if (i < 2 * kRedFloats) red[i / kRedFloats][i % kRedFloats] = 0.f;
+  for (int k = i + blockDim.x * blockDim.y; k < 2 * kRedFloats; k += blockDim.x * blockDim.y)
+    red[k / kRedFloats][k % kRedFloats] = 0.f;
+  __syncthreads();
 }
+
+// ---------------------------------------------------------------------------
+// how rows are split and fed
+// ---------------------------------------------------------------------------
+//
+// A row of H elements is split over TPR threads (whole warps) of CH 16-byte
+// pieces each, thread i taking the pieces i, i + TPR, ...: a function of H
+// and the type alone, so that a row's bits do not depend on the batch.  A CTA
+// holds several such groups, each walking over rows of its own.  A thread
+// copies its own pieces of the rows ahead into its own shared-memory slots
+// (cp.async, `depth` rows deep), so no barrier stands between a copy and its
+// use and the loads of later rows are in flight while a row waits for its sum.
+struct Split {
+  int ch, tpr;   // pieces a thread, threads a row
+};
+// `two`: the most pieces of a row that is split in two a thread.  Forward 896:
+// 448 threads at hidden = 7168 (M = 4096, E4M3) 38.9 us, four pieces for each of
+// 224 threads 47.1.  Gradient 512, up to 768 threads: at 896, with 72 registers
+// a thread instead of 80, hidden = 4096 (M = 10007) went from 55.6 to 71.4 us.
+Split split_row(int H, int per16, int two) {
+  const int pieces = (H + per16 - 1) / per16;
+  const int ch = pieces <= 256 ? 1 : pieces <= two ? 2 : pieces <= 2048 ? 4 : 8;
+  return Split{ch, ((pieces + ch - 1) / ch + 31) / 32 * 32};
+}
+constexpr int kTwoForward = 896, kTwoGradient = 512;
+
+// Rows in flight for a group so that an SM has about `flight` bytes in flight
+// with `groups` groups; no more than a group has rows (`turns`).
+int plan_depth(size_t stage, int groups, int64_t turns, int flight) {
+  const int64_t depth = flight / (int64_t)(stage * groups);
+  const int64_t most = turns < kMaxDepth ? turns : kMaxDepth;
+  return depth < 1 ? 1 : depth > most ? (int)most : (int)depth;
+}
+
+// The rows of IN input arrays (the last may be NULL: not used), as the walk
+// above feeds them (kWhole), or read straight from global memory.  In a stage
+// the slots of neighbouring threads are next to one another: copies and reads
+// of a warp are whole lines.  (Slots by thread, 112 bytes apart, took the
+// gradient at M = 10007, hidden = 4096 from 56 to 85 us.)
+template <typename T, int IN, int CH, int A>
+struct RowFeed {
+  static constexpr int N = kPer16<T>;
+  using TB = typename T::bits;
+  const TB *in[IN];
+  int64_t stride[IN];
+  int H, depth;
+  uint32_t at, first, last;   // this thread's slots: of the current stage, the ring's bounds
+
+  __device__ __forceinline__ uint32_t unit() const { return blockDim.x * blockDim.y * 16; }
+  __device__ __forceinline__ uint32_t stage_bytes() const {
+    return unit() * IN * CH;
+  }
+  __device__ __forceinline__ void init(uint4 *ring) {
+    const int flat = threadIdx.y * blockDim.x + threadIdx.x;
+    first = at = (uint32_t)__cvta_generic_to_shared(ring) + flat * 16;
+    last = first + depth * stage_bytes();
+  }
+  __device__ __forceinline__ bool used() const { return in[IN - 1] != nullptr; }
+  __device__ __forceinline__ bool on(int i) const {
+    return (int)(threadIdx.x + i * blockDim.x) < (H + N - 1) / N;
+  }
+  // Starts the copies of a row into the current stage (one group of copies,
+  // empty if !live) and moves on to the next stage.
+  __device__ __forceinline__ void start(int64_t row, bool live) {
+    if constexpr (A == kWhole) {
+      if (live) {
+#pragma unroll
+        for (int a = 0; a < IN; ++a) {
+          if (a == IN - 1 && !used()) continue;
+          const TB *p = in[a] + row * stride[a] + threadIdx.x * N;
+#pragma unroll
+          for (int i = 0; i < CH; ++i)
+            if (on(i)) copy16_async(at + (a * CH + i) * unit(), p + i * blockDim.x * N);
+        }
+      }
+      copies_commit();
+      at += stage_bytes();
+      if (at == last) at = first;
+    }
+  }
+  __device__ __forceinline__ void wait() const {
+    if constexpr (A == kWhole) copies_wait(depth);
+  }
+  // This thread's piece i (on(i)) of array a, row `row` in the current stage.
+  __device__ __forceinline__ Raw<T, N> get(int64_t row, int a, int i) const {
+    if constexpr (A == kWhole)
+      return raw_load_shared<T>(at + (a * CH + i) * unit());
+    else
+      return raw_load<T, N, A>(in[a] + row * stride[a], threadIdx.x + i * blockDim.x, H);
+  }
+};
+
+// The weights of a thread's pieces as fp32: in registers over all of its rows
+// where they are few, else read again (from L1) for every row.
+template <typename W, int N, int CH, int A>
+struct Weights {
+  static constexpr bool kHeld = CH * N <= 16;
+  f32x2 held[kHeld ? CH : 1][N / 2];
+
+  static __device__ __forceinline__ void read(const typename W::bits *w, int pieces, int H, int i,
+                                              f32x2 (&f)[N / 2]) {
+    const int c = threadIdx.x + i * blockDim.x;
+    raw_up<W, N>(c < pieces ? raw_load<W, N, A>(w, c, H) : raw_zero<W, N>(), f);
+  }
+  __device__ __forceinline__ void load(const typename W::bits *w, int pieces, int H) {
+    if constexpr (kHeld) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i) read(w, pieces, H, i, held[i]);
+    }
+  }
+  __device__ __forceinline__ void get(const typename W::bits *w, int pieces, int H, int i,
+                                      f32x2 (&f)[N / 2]) const {
+    if constexpr (kHeld) {
+#pragma unroll
+      for (int e = 0; e < N / 2; ++e) f[e] = held[i][e];
+    } else {
+      read(w, pieces, H, i, f);
+    }
+  }
+};
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
 //
 //   s = T(x + r);  rstd = 1 / sqrt(mean(s^2) + eps);  out = T(s * rstd * w)
-// and, by blocks of 128 columns with a = max |s * w|:
-//   scale = a * rstd / 448,  code = e4m3((s * w) * 448 / a).
+// and, by blocks of 128 columns with m = max |s * w|:
+//   scale = m * rstd / 448,  code = e4m3((s * w) * 448 / m).
 // The code's quotient leaves rstd out: for 16-bit s and w the product s * w
 // and its multiple by 448 = 7 * 64 are exact in fp32 (16 + 3 bits for bf16;
 // 22 + 3 for fp16, rounded once), so the only rounding ahead of the code is
-// the division's, and the codes do not depend on the order of the sum of
+// the quotient's, and the codes do not depend on the order of the sum of
 // squares.  Where the scale would be below 2^-126 it is 2^-126, so that no
-// scale is zero or subnormal.  A row is read once and kept in registers.
+// scale is zero or subnormal.
 
 struct NormArgs {
   const void *x, *r, *w;
   int64_t xs, rs;
-  int M, H;
-  float eps;
+  int M, H, depth;
+  float eps, inv_H;
   void *sum, *out;
   uint8_t *codes;
   float *scale, *rstd;
 };
 
-template <typename T, typename W, int CH, bool VEC>
-__global__ void __launch_bounds__(512) add_rmsnorm_kernel(NormArgs a) {
+// 448 * p / m for |p| <= m: with y = 1 / m rounded once, q = 448 p * y and its
+// residual 448 p - q m (one fma), q + residual * y is the quotient to within
+// its own rounding, and exact where the quotient is a float (a tie of the
+// code's rounding is); one division a block instead of one an element
+// (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990).  For m in [2^-100, 2^100], where neither the
+// residual nor y leaves the normal range.
+__device__ __forceinline__ f32x2 code_quotient(f32x2 p, f32x2 minus_m, f32x2 y) {
+  const f32x2 a = mul2(p, pair(kE4m3Max, kE4m3Max)), q = mul2(a, y);
+  return fma2(fma2(q, minus_m, a), y, q);
+}
+
+template <typename T, typename W, int CH, int A>
+__global__ void __launch_bounds__(CH <= 2 ? 448 : 512, CH <= 2 ? 2 : 1) add_rmsnorm_kernel(NormArgs a) {
   using TB = typename T::bits;
   using WB = typename W::bits;
-  __shared__ float red[kMaxWarps];
+  constexpr int N = kPer16<T>;
+  extern __shared__ uint4 ring[];
+  __shared__ __align__(16) float red[2][kRedFloats];
   pdl_wait();
   pdl_trigger();
-  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const bool live = row < a.M;
-  const int H = a.H, chunks = (H + kChunk - 1) / kChunk, tid = threadIdx.x, tpr = blockDim.x;
-  const TB *x = static_cast<const TB *>(a.x) + row * a.xs;
-  const TB *r = static_cast<const TB *>(a.r) + row * a.rs;
+  const int H = a.H, pieces = (H + N - 1) / N, tid = threadIdx.x, tpr = blockDim.x;
   const WB *w = static_cast<const WB *>(a.w);
-  Raw<T> xr[CH], rr[CH];
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  RowFeed<T, 2, CH, A> feed{{static_cast<const TB *>(a.x), static_cast<const TB *>(a.r)},
+                              {a.xs, a.rs},
+                              H,
+                              a.depth};
+  feed.init(ring);
+  for (int d = 0; d < a.depth; ++d) feed.start(row + d * step, row + d * step < a.M);
+  Weights<W, N, CH, A> weights;
+  weights.load(w, pieces, H);
+  clear_red(red);
+  int turn = 0;
+  for (; row < a.M; row += step) {
+    const size_t out_at = (size_t)row * H;
+    feed.wait();
+    Raw<T, N> sr[CH];
+    f32x2 sq = 0;
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int c = tid + i * tpr;
-    const bool on = live && c < chunks;
-    xr[i] = on ? raw_load<T, VEC>(x, c, H) : raw_zero<T>();
-    rr[i] = on && a.r ? raw_load<T, VEC>(r, c, H) : raw_zero<T>();
-  }
-  float s[CH][kChunk];
-  float sq = 0.f;
-#pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int c = tid + i * tpr;
-    raw_up<T>(xr[i], s[i]);
-    if (a.r) {
-      float f[kChunk];
-      raw_up<T>(rr[i], f);
-#pragma unroll
-      for (int e = 0; e < kChunk; ++e) f[e] += s[i][e];
-      xr[i] = raw_down<T>(f);   // the sum as it is stored is what is normalised
-      raw_up<T>(xr[i], s[i]);
-    }
-    if (a.sum && live && c < chunks)
-      raw_store<T, VEC>(static_cast<TB *>(a.sum) + row * H, c, H, xr[i]);
-#pragma unroll
-    for (int e = 0; e < kChunk; ++e) sq = fmaf(s[i][e], s[i][e], sq);
-  }
-  const float ms = group_sum(sq, red) / (float)H;
-  const float rstd = 1.f / sqrtf(ms + a.eps);
-  if (a.rstd && live && tid == 0) a.rstd[row] = rstd;
-  if (!a.out && !a.codes) return;
-#pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int c = tid + i * tpr;
-    const bool on = live && c < chunks;
-    float wf[kChunk];
-    raw_up<W>(c < chunks ? raw_load<W, VEC>(w, c, H) : raw_zero<W>(), wf);
-    if (a.out && on) {
-      float v[kChunk];
-#pragma unroll
-      for (int e = 0; e < kChunk; ++e) v[e] = s[i][e] * rstd * wf[e];
-      raw_store<T, VEC>(static_cast<TB *>(a.out) + row * H, c, H, raw_down<T>(v));
-    }
-    if (a.codes) {
-      float m = 0.f;
-#pragma unroll
-      for (int e = 0; e < kChunk; ++e) {
-        s[i][e] *= wf[e];
-        m = max_nan(m, fabsf(s[i][e]));
+    for (int i = 0; i < CH; ++i) {
+      sr[i] = raw_zero<T, N>();
+      if (feed.on(i)) {
+        sr[i] = feed.get(row, 0, i);
+        // the sum as it is stored is what is normalised
+        if (feed.used()) sr[i] = raw_add<T, N>(sr[i], feed.get(row, 1, i));
       }
-      // the sixteen threads of a block of 128 columns
+      if (a.sum)
+        raw_store<T, N, A>(static_cast<TB *>(a.sum) + out_at, tid + i * tpr, H, sr[i], feed.on(i));
+      f32x2 f[N / 2];
+      raw_up<T, N>(sr[i], f);
 #pragma unroll
-      for (int d = 8; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, d));
-      const float sc = m * rstd / kE4m3Max;
-      const bool low = sc < kScaleMin;
-      uint16_t q[4];
+      for (int e = 0; e < N / 2; ++e) sq = fma2(f[e], f[e], sq);
+    }
+    const float2 sq2 = unpair(sq);
+    const float ms = group_sum(sq2.x + sq2.y, red[turn]) * a.inv_H;
+    // the slots of this row have been read: the row `depth` turns on goes there
+    feed.start(row + a.depth * step, row + a.depth * step < a.M);
+    turn ^= 1;
+    const float rstd = 1.f / sqrtf(ms + a.eps);
+    if (a.rstd && tid == 0) a.rstd[row] = rstd;
+    if (!a.out && !a.codes) continue;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float v0 = s[i][2 * e], v1 = s[i][2 * e + 1];
-        v0 = low ? v0 * rstd / kScaleMin : v0 * kE4m3Max / m;
-        v1 = low ? v1 * rstd / kScaleMin : v1 * kE4m3Max / m;
-        q[e] = to_e4m3x2(v0, v1);
+    for (int i = 0; i < CH; ++i) {
+      const int c = tid + i * tpr;
+      const bool on = feed.on(i);
+      f32x2 f[N / 2], wf[N / 2];
+      raw_up<T, N>(sr[i], f);
+      weights.get(w, pieces, H, i, wf);
+      if (a.out) {
+        f32x2 v[N / 2];
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) v[e] = mul2(mul2(f[e], pair(rstd, rstd)), wf[e]);
+        raw_store<T, N, A>(static_cast<TB *>(a.out) + out_at, c, H, raw_down<T>(v), on);
       }
-      if (on) {
-        uint8_t *dst = a.codes + row * H + (size_t)c * kChunk;
-        const uint2 v = make_uint2(q[0] | ((uint32_t)q[1] << 16), q[2] | ((uint32_t)q[3] << 16));
-        if (VEC) {
-          *reinterpret_cast<uint2 *>(dst) = v;
-        } else {
-          const int left = H - c * kChunk;
+      if (a.codes) {
+        float m = 0.f;
 #pragma unroll
-          for (int e = 0; e < kChunk; ++e)
-            if (e < left) dst[e] = (uint8_t)((e < 4 ? v.x : v.y) >> (8 * (e & 3)));
+        for (int e = 0; e < N / 2; ++e) {
+          f[e] = mul2(f[e], wf[e]);
+          const float2 p = unpair(f[e]);
+          m = max_abs_nan(m, p.x, p.y);
         }
-        if ((tid & 15) == 0) a.scale[row * ((H + 127) / 128) + c / 16] = low ? kScaleMin : sc;
+        // the 128 / N threads of a block of 128 columns
+#pragma unroll
+        for (int d = 64 / N; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, d));
+        float sc = m * rstd / kE4m3Max;
+        if (sc >= kScaleMin && m >= 0x1p-100f && m <= 0x1p100f) {
+          const float y = 1.f / m;
+#pragma unroll
+          for (int e = 0; e < N / 2; ++e) f[e] = code_quotient(f[e], pair(-m, -m), pair(y, y));
+        } else {   // scales at their floor, and extremes of s * w
+          const bool low = sc < kScaleMin;
+#pragma unroll
+          for (int e = 0; e < N / 2; ++e) {
+            const float2 p = unpair(f[e]);
+            f[e] = low ? pair(p.x * rstd / kScaleMin, p.y * rstd / kScaleMin)
+                       : pair(p.x * kE4m3Max / m, p.y * kE4m3Max / m);
+          }
+          if (low) sc = kScaleMin;
+        }
+        uint32_t q[N / 4];
+#pragma unroll
+        for (int e = 0; e < N / 4; ++e) {
+          const float2 lo = unpair(f[2 * e]), hi = unpair(f[2 * e + 1]);
+          q[e] = to_e4m3x2(lo.x, lo.y) | ((uint32_t)to_e4m3x2(hi.x, hi.y) << 16);
+        }
+        if (on) {
+          uint8_t *dst = a.codes + out_at + (size_t)c * N;
+          if constexpr (A != kWhole) {
+            const int left = H - c * N;
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+              if (e < left) dst[e] = (uint8_t)(q[e / 4] >> (8 * (e & 3)));
+          } else if constexpr (N == 8) {
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(q[0], q[1]);
+          } else {
+            *reinterpret_cast<uint32_t *>(dst) = q[0];
+          }
+          if (tid % (128 / N) == 0) a.scale[row * ((H + 127) / 128) + c / (128 / N)] = sc;
+        }
       }
     }
   }
@@ -180,99 +339,125 @@ __global__ void __launch_bounds__(512) add_rmsnorm_kernel(NormArgs a) {
 //
 // With xh = s * rstd and g = dout * w:
 //   dx = T(rstd * (g - xh * mean(g * xh)) + dsum),  dw = sum_t dout[t] * xh[t].
-// A row group walks over its rows with their part of dw in registers; the
-// CTAs' parts go to the workspace [CTAs][H] and a second kernel adds them in
-// CTA order, so the bits are the same every time.
+// A group walks over its rows with their part of dw in registers; one CTA an
+// SM adds its groups' parts in order, the CTAs' parts go to the workspace
+// [CTAs][H] and a second kernel adds those in a fixed order, so the bits are
+// the same every time.
 
 struct NormGradArgs {
-  const void *dout, *sum, *w, *dsum;
+  const void *dout, *sum, *dsum, *w;
   const float *rstd;
-  int64_t ds, ss, dss;
-  int M, H;
+  int64_t ds, ss, es;
+  int M, H, depth;
+  float inv_H;
   void *dx;
-  float *part;   // [gridDim.x][H], or NULL: no dw
+  float *part;       // [gridDim.x][H], or NULL: no dw
 };
 
-template <typename T, typename W, int CH, bool VEC>
-__global__ void __launch_bounds__(512) rmsnorm_grad_kernel(NormGradArgs a) {
+// Threads of a CTA: as many as the registers of an SM hold.
+constexpr int grad_threads(int ch) { return ch <= 2 ? 768 : 512; }
+
+template <typename T, typename W, int CH, int A>
+__global__ void __launch_bounds__(grad_threads(CH)) rmsnorm_grad_kernel(NormGradArgs a) {
   using TB = typename T::bits;
   using WB = typename W::bits;
-  __shared__ float red[2][kMaxWarps];
-  extern __shared__ float parts[];   // [blockDim.y][H] when rows share a CTA
+  constexpr int N = kPer16<T>;
+  extern __shared__ uint4 ring[];
+  __shared__ __align__(16) float red[2][kRedFloats];
   pdl_wait();
   pdl_trigger();
-  const int H = a.H, chunks = (H + kChunk - 1) / kChunk, tid = threadIdx.x, tpr = blockDim.x;
+  const int H = a.H, pieces = (H + N - 1) / N, tid = threadIdx.x, tpr = blockDim.x;
   const WB *w = static_cast<const WB *>(a.w);
-  float dw[CH][kChunk] = {};
+  f32x2 dw[CH][N / 2] = {};
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  RowFeed<T, 3, CH, A> feed{{static_cast<const TB *>(a.dout), static_cast<const TB *>(a.sum),
+                               static_cast<const TB *>(a.dsum)},
+                              {a.ds, a.ss, a.es},
+                              H,
+                              a.depth};
+  feed.init(ring);
+  for (int d = 0; d < a.depth; ++d) feed.start(row + d * step, row + d * step < a.M);
+  Weights<W, N, CH, A> weights;
+  weights.load(w, pieces, H);
+  clear_red(red);
   int turn = 0;
-  // every group of the CTA makes the same number of turns: they share barriers
-  for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < a.M; r0 += step, turn ^= 1) {
-    const int64_t row = r0 + threadIdx.y;
-    const bool live = row < a.M;
-    const TB *d = static_cast<const TB *>(a.dout) + row * a.ds;
-    const TB *s = static_cast<const TB *>(a.sum) + row * a.ss;
-    const TB *ex = static_cast<const TB *>(a.dsum) + row * a.dss;
-    Raw<T> dr[CH], sr[CH], er[CH];
+  float next = row < a.M ? a.rstd[row] : 0.f;   // rstd, read a row ahead
+  for (; row < a.M; row += step) {
+    const size_t out_at = (size_t)row * H;
+    const float rstd = next;
+    next = row + step < a.M ? a.rstd[row + step] : 0.f;
+    const f32x2 rstd2 = pair(rstd, rstd);
+    feed.wait();
+    Raw<T, N> dr[CH], sr[CH];
+    f32x2 dot = 0;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = tid + i * tpr;
-      const bool on = live && c < chunks;
-      dr[i] = on ? raw_load<T, VEC>(d, c, H) : raw_zero<T>();
-      sr[i] = on ? raw_load<T, VEC>(s, c, H) : raw_zero<T>();
-      er[i] = on && a.dsum ? raw_load<T, VEC>(ex, c, H) : raw_zero<T>();
-    }
-    const float rstd = live ? a.rstd[row] : 0.f;
-    float dot = 0.f;
+      if (!feed.on(i)) {
+        if constexpr (A != kWhole) dr[i] = sr[i] = raw_zero<T, N>();
+        continue;
+      }
+      dr[i] = feed.get(row, 0, i);
+      sr[i] = feed.get(row, 1, i);
+      f32x2 d[N / 2], xh[N / 2], wf[N / 2];
+      raw_up<T, N>(dr[i], d);
+      raw_up<T, N>(sr[i], xh);
+      weights.get(w, pieces, H, i, wf);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = tid + i * tpr;
-      float df[kChunk], xh[kChunk], wf[kChunk];
-      raw_up<T>(dr[i], df);
-      raw_up<T>(sr[i], xh);
-      raw_up<W>(c < chunks ? raw_load<W, VEC>(w, c, H) : raw_zero<W>(), wf);
-#pragma unroll
-      for (int e = 0; e < kChunk; ++e) {
-        xh[e] *= rstd;
-        dw[i][e] = fmaf(df[e], xh[e], dw[i][e]);
-        dot = fmaf(df[e] * wf[e], xh[e], dot);
+      for (int e = 0; e < N / 2; ++e) {
+        xh[e] = mul2(xh[e], rstd2);
+        dw[i][e] = fma2(d[e], xh[e], dw[i][e]);
+        dot = fma2(mul2(d[e], wf[e]), xh[e], dot);
       }
     }
-    const float mean = group_sum(dot, red[turn]) / (float)H;
+    const float2 dot2 = unpair(dot);
+    const float mean = group_sum(dot2.x + dot2.y, red[turn]) * a.inv_H;
+    // dx = rstd * g + dsum - s * (rstd^2 * mean)
+    const float back = -(rstd * rstd * mean);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = tid + i * tpr;
-      if (!live || c >= chunks) continue;
-      float df[kChunk], xh[kChunk], wf[kChunk], ef[kChunk];
-      raw_up<T>(dr[i], df);
-      raw_up<T>(sr[i], xh);
-      raw_up<T>(er[i], ef);
-      raw_up<W>(raw_load<W, VEC>(w, c, H), wf);
+      if (A == kWhole && !feed.on(i)) continue;   // else whole warps up to the store
+      f32x2 d[N / 2], s[N / 2], wf[N / 2], v[N / 2] = {};
+      raw_up<T, N>(dr[i], d);
+      raw_up<T, N>(sr[i], s);
+      if (feed.used() && feed.on(i)) raw_up<T, N>(feed.get(row, 2, i), v);
+      weights.get(w, pieces, H, i, wf);
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e)
-        ef[e] = fmaf(rstd, df[e] * wf[e] - xh[e] * rstd * mean, ef[e]);
-      raw_store<T, VEC>(static_cast<TB *>(a.dx) + row * H, c, H, raw_down<T>(ef));
+      for (int e = 0; e < N / 2; ++e)
+        v[e] = fma2(s[e], pair(back, back), fma2(rstd2, mul2(d[e], wf[e]), v[e]));
+      raw_store<T, N, A>(static_cast<TB *>(a.dx) + out_at, tid + i * tpr, H, raw_down<T>(v), feed.on(i));
     }
+    // the slots of this row have been read: the row `depth` turns on goes there
+    feed.start(row + a.depth * step, row + a.depth * step < a.M);
+    turn ^= 1;
   }
   if (!a.part) return;
   float *part = a.part + (size_t)blockIdx.x * H;
-  if (blockDim.y == 1) {
+  // the groups' parts are added in shared memory, in the ring's place
+  const bool shared = blockDim.y > 1;
+  float *parts = reinterpret_cast<float *>(ring);
+  copies_wait(1);
+  if (shared) __syncthreads();
+  float *mine = shared ? parts + threadIdx.y * H : part;
 #pragma unroll
-    for (int i = 0; i < CH; ++i)
+  for (int i = 0; i < CH; ++i) {
+    const int h = (tid + i * tpr) * N;
+    if (A == kWhole) {
+      if (h < H)
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e) {
-        const int h = (tid + i * tpr) * kChunk + e;
-        if (h < H) part[h] = dw[i][e];
+        for (int e = 0; e < N / 4; ++e)
+          *reinterpret_cast<ulonglong2 *>(mine + h + 4 * e) =
+              make_ulonglong2(dw[i][2 * e], dw[i][2 * e + 1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N / 2; ++e) {
+        const float2 v = unpair(dw[i][e]);
+        if (h + 2 * e < H) mine[h + 2 * e] = v.x;
+        if (h + 2 * e + 1 < H) mine[h + 2 * e + 1] = v.y;
       }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < CH; ++i)
-#pragma unroll
-    for (int e = 0; e < kChunk; ++e) {
-      const int h = (tid + i * tpr) * kChunk + e;
-      if (h < H) parts[threadIdx.y * H + h] = dw[i][e];
     }
+  }
+  if (!shared) return;
   __syncthreads();
   for (int h = threadIdx.y * tpr + tid; h < H; h += tpr * blockDim.y) {
     float v = parts[h];
@@ -281,33 +466,41 @@ __global__ void __launch_bounds__(512) rmsnorm_grad_kernel(NormGradArgs a) {
   }
 }
 
-// dw[h] = sum over the CTAs' parts: 32 columns a CTA, 16 threads a column
-// that take every sixteenth part, then those sixteen in order.
-constexpr int kSumRows = 16;
-__global__ void __launch_bounds__(32 * kSumRows) sum_parts_kernel(const float *part, int n, int H,
-                                                                  float *dw) {
-  __shared__ float red[kSumRows][32];
+// dw[h] = sum over the CTAs' parts: 32 columns a CTA, 32 threads a column that
+// take every 32nd part (eight loads in flight), then a butterfly over those.
+__global__ void __launch_bounds__(1024) sum_parts_kernel(const float *part, int n, int H,
+                                                         float *dw) {
+  __shared__ float red[32][33];
   pdl_wait();
   pdl_trigger();
-  const int h = blockIdx.x * 32 + threadIdx.x;
+  const int x = threadIdx.x, y = threadIdx.y, h = blockIdx.x * 32 + x;
   float v = 0.f;
-  if (h < H)
-    for (int i = threadIdx.y; i < n; i += kSumRows) v += __ldcg(part + (size_t)i * H + h);
-  red[threadIdx.y][threadIdx.x] = v;
-  __syncthreads();
-  if (threadIdx.y == 0 && h < H) {
-    for (int i = 1; i < kSumRows; ++i) v += red[i][threadIdx.x];
-    dw[h] = v;
+  if (h < H) {
+#pragma unroll 8
+    for (int i = y; i < n; i += 32) v += __ldcg(part + (size_t)i * H + h);
   }
+  red[y][x] = v;
+  __syncthreads();
+  v = red[x][y];   // column y of the CTA, its x-th sum
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+  if (x == 0 && blockIdx.x * 32 + y < H) dw[blockIdx.x * 32 + y] = v;
 }
 
-constexpr int kGradCtas = 456;   // most CTAs of the gradient: three for each of 152 SMs
-constexpr int kGradThreads = 256;
+constexpr int kSms = 152;
 
-// CTAs of the gradient for M rows.
-int grad_ctas(int M, const Split &s) {
-  const int64_t want = ceil_div64(M, s.rows);
-  return want < kGradCtas ? (int)want : kGradCtas;
+// The walk of the gradient over M rows: one CTA an SM (a constant, not the
+// device's count: dw's order depends on M, hidden and the type alone), as many
+// groups in it as its threads allow and the rows need.
+struct Walk {
+  int ctas, groups;
+};
+Walk grad_walk(int M, const Split &s) {
+  const int64_t want = ceil_div64(M, kSms);
+  const int fit = grad_threads(s.ch) / s.tpr;
+  const int groups = want < 1 ? 1 : want < fit ? (int)want : fit;
+  const int64_t ctas = ceil_div64(M, groups);
+  return Walk{ctas < kSms ? (int)ctas : kSms, groups};
 }
 
 template <typename F>
@@ -326,7 +519,7 @@ bool float_dtype(int d) {
 
 int norm_sizes(int dtype, int weight_dtype, int M, int H) {
   if (!float_dtype(dtype) || !float_dtype(weight_dtype) || M < 0 || H < 1) return MOE_EINVAL;
-  if (H > MOE_MAX_NORM_HIDDEN) return MOE_EUNSUPPORTED;
+  if (H > MOE_MAX_ROW_HIDDEN) return MOE_EUNSUPPORTED;
   return with_norm_types(dtype, weight_dtype, [](auto, auto) { return MOE_OK; });
 }
 
@@ -367,29 +560,54 @@ extern "C" int moe_add_rmsnorm(const void *x, int64_t x_stride, const void *resi
                                    out_scale, rstd);
   if (st || M == 0) return st;
   const int b = dtype_bytes(dtype), wb = dtype_bytes(weight_dtype);
-  const bool vec = hidden % kChunk == 0 && rows_vector(x, x_stride, b) &&
-                   rows_vector(residual, residual_stride, b) && rows_vector(sum_out, hidden, b) &&
-                   rows_vector(out, hidden, b) && rows_vector(weight, hidden, wb) &&
-                   ((uintptr_t)out_codes & 7) == 0;
-  const Split s = split_row(hidden, 128);
-  const NormArgs a{x,      residual, weight, x_stride, residual_stride, M,    hidden,
-                   eps,    sum_out,  out,    out_codes, out_scale,      rstd};
-  const dim3 grid((unsigned)ceil_div64(M, s.rows)), block(s.tpr, s.rows);
+  const int n = 16 / b;   // elements of a piece
+  int align = rows_alignment(x, x_stride, hidden, b);
+  for (const int k : {rows_alignment(residual, residual_stride, hidden, b),
+                      rows_alignment(sum_out, hidden, hidden, b),
+                      rows_alignment(out, hidden, hidden, b),
+                      rows_alignment(weight, hidden, hidden, wb)})
+    if (k < align) align = k;
+  if ((uintptr_t)out_codes % n && align == kWhole) align = kHalves;
+  // CTAs of about 256 threads, as many as an SM's registers hold (72 a thread,
+  // 128 with four pieces and more)
+  const Split s = split_row(hidden, n, kTwoForward);
+  const int rows = s.tpr >= 256 ? 1 : 256 / s.tpr;
+  const int resident = (s.ch <= 2 ? 896 : 512) / (s.tpr * rows);
+  const int64_t turns = ceil_div64(M, rows), most = (int64_t)sm_count() * resident;
+  const int64_t ctas = turns < most ? turns : most;
+  // 64 KB in flight an SM: at M = 32768, hidden = 4096 in bf16 162 us, but
+  // 192 us with 128 KB (the reads crowd out the writes)
+  const size_t stage = (size_t)2 * s.ch * s.tpr * rows * 16;
+  const int depth = plan_depth(stage, resident, ceil_div64(turns, ctas), 64 * 1024);
+  const NormArgs a{x,   residual, weight,    x_stride,  residual_stride, M, hidden, depth,
+                   eps, 1.f / hidden, sum_out, out, out_codes, out_scale, rstd};
+  const dim3 grid((unsigned)ctas), block(s.tpr, rows);
+  const size_t smem = align == kWhole ? depth * stage : 0;
   return with_norm_types(dtype, weight_dtype, [&](auto t, auto w) {
     using T = decltype(t);
     using W = decltype(w);
-    auto go = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, stream, a); };
-    if (s.ch == 1) return vec ? go(add_rmsnorm_kernel<T, W, 1, true>) : go(add_rmsnorm_kernel<T, W, 1, false>);
-    if (s.ch == 2) return vec ? go(add_rmsnorm_kernel<T, W, 2, true>) : go(add_rmsnorm_kernel<T, W, 2, false>);
-    return vec ? go(add_rmsnorm_kernel<T, W, 4, true>) : go(add_rmsnorm_kernel<T, W, 4, false>);
+    auto go = [&](auto kernel) {
+      const int rc = ensure_smem_limit((const void *)kernel, smem + kStaticBytes);
+      return rc ? rc : launch_pdl(kernel, grid, block, smem, stream, a);
+    };
+    if (s.ch == 1) return by_align(
+          align, [&](auto al) { return go(add_rmsnorm_kernel<T, W, 1, decltype(al)::value>); });
+    if (s.ch == 2) return by_align(
+          align, [&](auto al) { return go(add_rmsnorm_kernel<T, W, 2, decltype(al)::value>); });
+    if (s.ch == 4) return by_align(
+          align, [&](auto al) { return go(add_rmsnorm_kernel<T, W, 4, decltype(al)::value>); });
+    if constexpr (sizeof(typename T::bits) == 4)   // fp32 rows above 8192
+      return by_align(
+          align, [&](auto al) { return go(add_rmsnorm_kernel<T, W, 8, decltype(al)::value>); });
+    return MOE_EUNSUPPORTED;
   });
 }
 
 extern "C" size_t moe_add_rmsnorm_backward_workspace_bytes(int M, int hidden) {
-  if (M < 0 || hidden < 1 || hidden > MOE_MAX_NORM_HIDDEN) return 0;
-  const moe::Split s = moe::split_row(hidden, moe::kGradThreads);
-  const int ctas = moe::grad_ctas(M, s);
-  return (size_t)(ctas > 0 ? ctas : 1) * hidden * sizeof(float);
+  if (M < 0 || hidden < 1 || hidden > MOE_MAX_ROW_HIDDEN) return 0;
+  // of the most CTAs that M rows or fewer take
+  const int ctas = M < 1 ? 1 : M < moe::kSms ? M : moe::kSms;
+  return (size_t)ctas * hidden * sizeof(float);
 }
 
 extern "C" int moe_add_rmsnorm_backward(const void *dout, int64_t dout_stride, const void *sum,
@@ -414,28 +632,48 @@ extern "C" int moe_add_rmsnorm_backward(const void *dout, int64_t dout_stride, c
   if ((dout_stride != hidden && dout == dx) || (sum_stride != hidden && sum == dx) ||
       (dsum && dsum_stride != hidden && dsum == dx))
     return MOE_EINVAL;
-  const Split s = split_row(hidden, kGradThreads);
-  const int ctas = grad_ctas(M, s);
+  const int n = 16 / b;
+  const Split s = split_row(hidden, n, kTwoGradient);
+  int align = rows_alignment(dout, dout_stride, hidden, b);
+  for (const int k : {rows_alignment(sum, sum_stride, hidden, b),
+                      rows_alignment(dsum, dsum_stride, hidden, b),
+                      rows_alignment(dx, hidden, hidden, b),
+                      rows_alignment(weight, hidden, hidden, wb)})
+    if (k < align) align = k;
+  const Walk walk = grad_walk(M, s);
   float *part = dweight ? static_cast<float *>(workspace) : nullptr;
   if (M > 0) {
-    const bool vec = hidden % kChunk == 0 && rows_vector(dout, dout_stride, b) &&
-                     rows_vector(sum, sum_stride, b) && rows_vector(dsum, dsum_stride, b) &&
-                     rows_vector(dx, hidden, b) && rows_vector(weight, hidden, wb);
-    const NormGradArgs a{dout,        sum, weight, dsum, rstd, dout_stride, sum_stride,
-                         dsum_stride, M,   hidden, dx,   part};
-    const dim3 grid(ctas), block(s.tpr, s.rows);
-    const size_t smem = s.rows > 1 ? (size_t)s.rows * hidden * sizeof(float) : 0;
+    const size_t stage = (size_t)3 * s.ch * s.tpr * walk.groups * 16;
+    const int64_t turns = ceil_div64(M, (int64_t)walk.ctas * walk.groups);
+    const int depth = plan_depth(stage, 1, turns, 144 * 1024);
+    const size_t ring = align == kWhole ? depth * stage : 0;
+    const size_t parts = walk.groups > 1 ? (size_t)walk.groups * hidden * sizeof(float) : 0;
+    const size_t smem = ring > parts ? ring : parts;
+    const NormGradArgs a{dout, sum,    dsum,  weight, rstd, dout_stride, sum_stride, dsum_stride,
+                         M,    hidden, depth, 1.f / hidden, dx, part};
+    const dim3 grid(walk.ctas), block(s.tpr, walk.groups);
     const int rc = with_norm_types(dtype, weight_dtype, [&](auto t, auto w) {
       using T = decltype(t);
       using W = decltype(w);
-      auto go = [&](auto kernel) { return launch_pdl(kernel, grid, block, smem, stream, a); };
-      if (s.ch == 1) return vec ? go(rmsnorm_grad_kernel<T, W, 1, true>) : go(rmsnorm_grad_kernel<T, W, 1, false>);
-      if (s.ch == 2) return vec ? go(rmsnorm_grad_kernel<T, W, 2, true>) : go(rmsnorm_grad_kernel<T, W, 2, false>);
-      return vec ? go(rmsnorm_grad_kernel<T, W, 4, true>) : go(rmsnorm_grad_kernel<T, W, 4, false>);
+      auto go = [&](auto kernel) {
+        const int r = ensure_smem_limit((const void *)kernel, smem + kStaticBytes);
+        return r ? r : launch_pdl(kernel, grid, block, smem, stream, a);
+      };
+      if (s.ch == 1) return by_align(
+          align, [&](auto al) { return go(rmsnorm_grad_kernel<T, W, 1, decltype(al)::value>); });
+      if (s.ch == 2) return by_align(
+          align, [&](auto al) { return go(rmsnorm_grad_kernel<T, W, 2, decltype(al)::value>); });
+      if (s.ch == 4) return by_align(
+          align, [&](auto al) { return go(rmsnorm_grad_kernel<T, W, 4, decltype(al)::value>); });
+      if constexpr (sizeof(typename T::bits) == 4)   // fp32 rows above 8192
+        return by_align(
+          align, [&](auto al) { return go(rmsnorm_grad_kernel<T, W, 8, decltype(al)::value>); });
+      return MOE_EUNSUPPORTED;
     });
     if (rc) return rc;
   }
   if (!dweight) return MOE_OK;
-  return launch_pdl(sum_parts_kernel, dim3((hidden + 31) / 32), dim3(32, kSumRows), 0, stream,
-                    (const float *)part, ctas, hidden, dweight);
+  if (const int r = ensure_max_carveout((const void *)sum_parts_kernel)) return r;
+  return launch_pdl(sum_parts_kernel, dim3((hidden + 31) / 32), dim3(32, 32), 0, stream,
+                    (const float *)part, M > 0 ? walk.ctas : 0, hidden, dweight);
 }

@@ -1,17 +1,48 @@
-// rows.cuh -- rows of 16- or 32-bit floats in chunks of eight, for the
-// row-wise kernels (token dispatch and combination, RMS norm): raw loads and
-// stores, and the exact or once-rounded conversions to and from fp32.
+// rows.cuh -- rows of 16- or 32-bit floats in pieces of a few elements, for
+// the row-wise kernels (token dispatch and combination, RMS norm): raw loads
+// and stores, and the exact or once-rounded conversions to and from fp32.
 #pragma once
+
+#include <type_traits>
 
 #include "common.cuh"
 
 namespace moe {
 
-// The storage types of token and expert rows.
+// Two floats in one 64-bit register pair, the first in the low half: the
+// packed fp32 instructions of sm_100 do both lanes in one issue, each rounded
+// like the plain one.
+using f32x2 = uint64_t;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(f32x2 v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// The storage types of token and expert rows.  add: the sum of the elements of
+// one 32-bit word, rounded once.
 struct BF16 {
   using bits = uint16_t;
-  static __device__ __forceinline__ float up(uint16_t b) { return bf16_to_float(b); }
-  static __device__ __forceinline__ uint16_t down(float f) { return float_to_bf16_rn(f); }
+  static __device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
   // two floats, the first in the low half
   static __device__ __forceinline__ uint32_t down2(float lo, float hi) {
     uint32_t r;
@@ -24,14 +55,9 @@ struct BF16 {
 };
 struct F16 {
   using bits = uint16_t;
-  static __device__ __forceinline__ float up(uint16_t b) {
-    float f;
-    asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(b));
-    return f;
-  }
-  static __device__ __forceinline__ uint16_t down(float f) {
-    uint16_t r;
-    asm("cvt.rn.f16.f32 %0, %1;" : "=h"(r) : "f"(f));
+  static __device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
   }
   static __device__ __forceinline__ uint32_t down2(float lo, float hi) {
@@ -43,116 +69,306 @@ struct F16 {
 };
 struct F32 {
   using bits = uint32_t;
-  static __device__ __forceinline__ float up(uint32_t b) { return __uint_as_float(b); }
-  static __device__ __forceinline__ uint32_t down(float f) { return __float_as_uint(f); }
+  static __device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }
 };
 
-constexpr int kChunk = 8;   // elements a thread takes at a time
-
-// Eight elements as they are stored: one 16-byte register quad, or two.
+// Elements of T in the 16 bytes that a thread moves at a time.
 template <typename T>
+constexpr int kPer16 = 16 / (int)sizeof(typename T::bits);
+
+// N consecutive elements as they are stored, in 32-bit words.
+template <typename T, int N>
 struct Raw {
-  static constexpr int kQuads = (int)sizeof(typename T::bits) * kChunk / 16;
-  uint4 q[kQuads];
+  static constexpr int kWords = N * (int)sizeof(typename T::bits) / 4;
+  uint32_t w[kWords];
 };
 
-template <typename T>
-__device__ __forceinline__ Raw<T> raw_zero() {
-  Raw<T> r;
+template <typename T, int N>
+__device__ __forceinline__ Raw<T, N> raw_zero() {
+  Raw<T, N> r;
 #pragma unroll
-  for (int i = 0; i < Raw<T>::kQuads; ++i) r.q[i] = make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < Raw<T, N>::kWords; ++i) r.w[i] = 0;
   return r;
 }
 
-// Chunk c of a row of H elements.  VEC: the row is 16-byte aligned and H is a
-// multiple of 8.  Otherwise element by element, zeros behind the end.  Plain
-// (coherent) loads: some callers let an output share an input's buffer.
-template <typename T, bool VEC>
-__device__ __forceinline__ Raw<T> raw_load(const typename T::bits *row, int c, int H) {
-  Raw<T> r;
-  if (VEC) {
-    const uint4 *p = reinterpret_cast<const uint4 *>(row + (size_t)c * kChunk);
-#pragma unroll
-    for (int i = 0; i < Raw<T>::kQuads; ++i) r.q[i] = p[i];
+// The N elements at p, aligned to their bytes (at most 16).
+template <typename T, int N>
+__device__ __forceinline__ Raw<T, N> raw_load_aligned(const void *p) {
+  constexpr int W = Raw<T, N>::kWords;
+  Raw<T, N> r;
+  if constexpr (W == 2) {
+    const uint2 v = *static_cast<const uint2 *>(p);
+    r.w[0] = v.x;
+    r.w[1] = v.y;
   } else {
-    const typename T::bits *p = row + (size_t)c * kChunk;
-    const int left = H - c * kChunk;
-    uint32_t w[Raw<T>::kQuads * 4];
-    if (sizeof(typename T::bits) == 2) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = 2 * i < left ? (uint32_t)p[2 * i] : 0u;
-        const uint32_t hi = 2 * i + 1 < left ? (uint32_t)p[2 * i + 1] : 0u;
-        w[i] = lo | (hi << 16);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i) w[i % (Raw<T>::kQuads * 4)] = i < left ? (uint32_t)p[i] : 0u;
+    for (int i = 0; i < W / 4; ++i) {
+      const uint4 v = static_cast<const uint4 *>(p)[i];
+      r.w[4 * i] = v.x;
+      r.w[4 * i + 1] = v.y;
+      r.w[4 * i + 2] = v.z;
+      r.w[4 * i + 3] = v.w;
     }
-#pragma unroll
-    for (int i = 0; i < Raw<T>::kQuads; ++i)
-      r.q[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
   }
   return r;
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void raw_store(typename T::bits *row, int c, int H, const Raw<T> &r) {
-  if (VEC) {
-    uint4 *p = reinterpret_cast<uint4 *>(row + (size_t)c * kChunk);
+// ---- pieces by alignment ------------------------------------------------------
+//
+// How the pieces of a call's rows can be moved: whole (16-byte aligned rows of
+// whole pieces), as 8-byte halves (8-byte aligned, a multiple of 8 bytes), or
+// element by element.
+enum { kWhole = 16, kHalves = 8, kElems = 1 };
+
+// Bytes [n, n + 16) of the 32 bytes lo, hi; 0 <= n < 16.
+__device__ __forceinline__ uint4 bytes_from(const uint4 &lo, const uint4 &hi, int n) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (n & 8) {
 #pragma unroll
-    for (int i = 0; i < Raw<T>::kQuads; ++i) p[i] = r.q[i];
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (n & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  const int s = (n & 3) * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s),
+                    __funnelshift_r(w[2], w[3], s), __funnelshift_r(w[3], w[4], s));
+}
+
+template <int ES> struct Elem;
+template <> struct Elem<1> { using type = uint8_t; };
+template <> struct Elem<2> { using type = uint16_t; };
+template <> struct Elem<4> { using type = uint32_t; };
+
+// Element i (of ES bytes) of a piece.
+template <int ES>
+__device__ __forceinline__ typename Elem<ES>::type elem_of(const uint4 &q, int i) {
+  const int b = i * ES;
+  const uint32_t w = b / 4 == 0 ? q.x : b / 4 == 1 ? q.y : b / 4 == 2 ? q.z : q.w;
+  return (typename Elem<ES>::type)(w >> (8 * (b & 3)));
+}
+
+// The 16 bytes at byte `at` (a multiple of 16) of a row of `len` bytes, zeros
+// behind its end.
+template <int ES, int A>
+__device__ __forceinline__ uint4 load16(const void *row, int at, int len) {
+  const char *p = static_cast<const char *>(row) + at;
+  if constexpr (A == kWhole) {
+    return *reinterpret_cast<const uint4 *>(p);
+  } else if constexpr (A == kHalves) {
+    const uint2 lo = *reinterpret_cast<const uint2 *>(p);
+    const uint2 hi = at + 8 < len ? reinterpret_cast<const uint2 *>(p)[1] : make_uint2(0, 0);
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
   } else {
-    typename T::bits *p = row + (size_t)c * kChunk;
-    const int left = H - c * kChunk;
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      if (i >= left) continue;
-      constexpr int per = 4 / (int)sizeof(typename T::bits);   // elements per 32-bit word
-      const uint4 q = r.q[i / (4 * per)];
-      const int k = (i / per) & 3;
-      const uint32_t w = k == 0 ? q.x : k == 1 ? q.y : k == 2 ? q.z : q.w;
-      p[i] = (typename T::bits)(per == 2 && (i & 1) ? w >> 16 : w);
+    for (int i = 0; i < 16 / ES; ++i)
+      if (at + i * ES < len)
+        w[i * ES / 4] |= (uint32_t)reinterpret_cast<const typename Elem<ES>::type *>(p)[i]
+                         << (8 * (i * ES & 3));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Writes 16 bytes q at byte `at` of a row that is moved element by element:
+// what lies inside the row, nothing outside.  A whole warp, whose lanes hold
+// consecutive pieces; lanes that are not `on`, the last ones, hold none.  A
+// piece lies across two aligned 16-byte windows: the lanes hand their ends on
+// and write by window, single elements only at the ends of the row and of the
+// warp (the combine gradient's fp16 rows of 2884: 117 us by elements, 81 by
+// windows).  Not inlined: the callers' unrolled loops hold eight of them.
+template <int ES>
+__device__ __noinline__ void store16_elems(void *row, int at, int len, uint4 q, bool on) {
+  using E = typename Elem<ES>::type;
+  char *p = static_cast<char *>(row) + at;
+  const int off = (int)((uintptr_t)row & 15);   // the warp's: `at` is a multiple of 16
+  const int mine = len - at < 16 ? len - at : 16;   // bytes of the piece
+  const int lane = threadIdx.x & 31, head = 16 - off;   // the piece's bytes in its first window
+  int from = 16, to = mine;   // what is written by elements
+  if (off == 0) {
+    if (!on) return;
+    if (mine == 16)
+      *reinterpret_cast<uint4 *>(p) = q;
+    else
+      from = 0;
+  } else {
+    uint4 prev;
+    prev.x = __shfl_up_sync(0xFFFFFFFFu, q.x, 1);
+    prev.y = __shfl_up_sync(0xFFFFFFFFu, q.y, 1);
+    prev.z = __shfl_up_sync(0xFFFFFFFFu, q.z, 1);
+    prev.w = __shfl_up_sync(0xFFFFFFFFu, q.w, 1);
+    if (!on) return;
+    const bool last = lane == 31 || at + 16 >= len;   // no lane takes this one's tail
+    if (lane == 0) {
+      from = 0;   // its window is shared with the warp before
+      if (!last && to > head) to = head;
+    } else if (mine >= head) {
+      *reinterpret_cast<uint4 *>(p - off) = bytes_from(prev, q, head);
+      if (last) from = head;
+    } else {   // the row ends in the window: the neighbour's tail, too
+      from = 0;
+#pragma unroll
+      for (int i = 0; i < 16 / ES; ++i)
+        if (i * ES >= head) reinterpret_cast<E *>(p - 16)[i] = elem_of<ES>(prev, i);
     }
+  }
+  if (from < to) {
+#pragma unroll
+    for (int i = 0; i < 16 / ES; ++i)
+      if (i * ES >= from && i * ES < to) reinterpret_cast<E *>(p)[i] = elem_of<ES>(q, i);
+  }
+}
+
+template <int ES, int A>
+__device__ __forceinline__ void store16(void *row, int at, int len, const uint4 &q, bool on) {
+  char *p = static_cast<char *>(row) + at;
+  if constexpr (A == kWhole) {
+    if (on) *reinterpret_cast<uint4 *>(p) = q;
+  } else if constexpr (A == kHalves) {
+    if (on) *reinterpret_cast<uint2 *>(p) = make_uint2(q.x, q.y);
+    if (on && at + 8 < len) reinterpret_cast<uint2 *>(p)[1] = make_uint2(q.z, q.w);
+  } else {
+    store16_elems<ES>(row, at, len, q, on);
+  }
+}
+
+// Piece c (N elements, 16 bytes, or 8 in the 16-bit type of a mixed pair) of a
+// row of H elements; zeros behind the end.  Plain (coherent) loads: some
+// callers let an output share an input's buffer.
+template <typename T, int N, int A>
+__device__ __forceinline__ Raw<T, N> raw_load(const typename T::bits *row, int c, int H) {
+  constexpr int ES = sizeof(typename T::bits);
+  if constexpr (N * ES == 16) {
+    const uint4 q = load16<ES, A>(row, c * 16, H * ES);
+    return Raw<T, N>{{q.x, q.y, q.z, q.w}};
+  } else if constexpr (A == kWhole) {
+    return raw_load_aligned<T, N>(row + (size_t)c * N);
+  } else {
+    Raw<T, N> r = raw_zero<T, N>();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (c * N + i < H) r.w[i * ES / 4] |= (uint32_t)row[(size_t)c * N + i] << (8 * (i * ES & 3));
+    return r;
+  }
+}
+
+// kElems: a whole warp, as store16_elems.
+template <typename T, int N, int A>
+__device__ __forceinline__ void raw_store(typename T::bits *row, int c, int H, const Raw<T, N> &r,
+                                          bool on) {
+  constexpr int ES = sizeof(typename T::bits);
+  typename T::bits *p = row + (size_t)c * N;
+  if constexpr (N * ES == 16) {
+    store16<ES, A>(row, c * 16, H * ES, make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]), on);
+  } else if constexpr (A == kWhole) {
+    if (on) *reinterpret_cast<uint2 *>(p) = make_uint2(r.w[0], r.w[1]);
+  } else if (on) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (c * N + i < H) p[i] = (typename T::bits)(r.w[i * ES / 4] >> (8 * (i * ES & 3)));
   }
 }
 
 // Exact.
-template <typename T>
-__device__ __forceinline__ void raw_up(const Raw<T> &r, float (&f)[kChunk]) {
+template <typename T, int N>
+__device__ __forceinline__ void raw_up(const Raw<T, N> &r, float (&f)[N]) {
   if constexpr (sizeof(typename T::bits) == 2) {
-    const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = T::up2(w[i]);
+    for (int i = 0; i < N / 2; ++i) {
+      const float2 v = T::up2(r.w[i]);
       f[2 * i] = v.x;
       f[2 * i + 1] = v.y;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      f[4 * i] = __uint_as_float(r.q[i].x);
-      f[4 * i + 1] = __uint_as_float(r.q[i].y);
-      f[4 * i + 2] = __uint_as_float(r.q[i].z);
-      f[4 * i + 3] = __uint_as_float(r.q[i].w);
+    for (int i = 0; i < N; ++i) f[i] = __uint_as_float(r.w[i]);
+  }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void raw_up(const Raw<T, N> &r, f32x2 (&f)[N / 2]) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    if constexpr (sizeof(typename T::bits) == 2) {
+      const float2 v = T::up2(r.w[i]);
+      f[i] = pair(v.x, v.y);
+    } else {
+      f[i] = pair(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
     }
   }
 }
 
-// Rounded to nearest, ties to even.
-template <typename T>
-__device__ __forceinline__ Raw<T> raw_down(const float (&f)[kChunk]) {
-  Raw<T> r;
-  if constexpr (sizeof(typename T::bits) == 2) {
-    r.q[0] = make_uint4(T::down2(f[0], f[1]), T::down2(f[2], f[3]), T::down2(f[4], f[5]),
-                        T::down2(f[6], f[7]));
-  } else {
+template <typename T, int N>
+__device__ __forceinline__ Raw<T, N> raw_add(const Raw<T, N> &a, const Raw<T, N> &b) {
+  Raw<T, N> r;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      r.q[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
-                          __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3]));
+  for (int i = 0; i < Raw<T, N>::kWords; ++i) r.w[i] = T::add(a.w[i], b.w[i]);
+  return r;
+}
+
+// Rounded to nearest, ties to even.
+template <typename T, int P>
+__device__ __forceinline__ Raw<T, 2 * P> raw_down(const f32x2 (&f)[P]) {
+  Raw<T, 2 * P> r;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const float2 v = unpair(f[i]);
+    if constexpr (sizeof(typename T::bits) == 2) {
+      r.w[i] = T::down2(v.x, v.y);
+    } else {
+      r.w[2 * i] = __float_as_uint(v.x);
+      r.w[2 * i + 1] = __float_as_uint(v.y);
+    }
   }
   return r;
+}
+template <typename T, int N>
+__device__ __forceinline__ Raw<T, N> raw_down(const float (&f)[N]) {
+  Raw<T, N> r;
+  if constexpr (sizeof(typename T::bits) == 2) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) r.w[i] = T::down2(f[2 * i], f[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.w[i] = __float_as_uint(f[i]);
+  }
+  return r;
+}
+
+// ---- copies ahead (cp.async) ------------------------------------------------
+//
+// A thread copies pieces of rows that it will need into shared-memory slots of
+// its own, one group of copies at a time, and waits for the oldest group: no
+// barrier, no register holds what is in flight, and the wait ends with the
+// copies themselves.
+
+constexpr int kMaxDepth = 4;            // groups in flight
+constexpr size_t kStaticBytes = 20480;  // more than a kernel's other shared memory, with which
+                                        // the ring shares its limit
+
+__device__ __forceinline__ void copy16_async(uint32_t shared, const void *global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(shared), "l"(global) : "memory");
+}
+// The 16 bytes at a shared-memory address.
+template <typename T>
+__device__ __forceinline__ Raw<T, kPer16<T>> raw_load_shared(uint32_t shared) {
+  Raw<T, kPer16<T>> r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+               : "r"(shared)
+               : "memory");
+  return r;
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most depth - 1 of this thread's committed groups are in flight.
+__device__ __forceinline__ void copies_wait(int depth) {
+  if (depth >= 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // ---- host ------------------------------------------------------------------
@@ -167,11 +383,23 @@ inline int dtype_bytes(int dtype) {
   }
 }
 
-// Whether rows of `hidden` elements at p, `stride` elements apart, can be
-// read and written in 16-byte pieces (NULL: not used).
-inline bool rows_vector(const void *p, int64_t stride, int bytes) {
-  return !p || (((uintptr_t)p & 15) == 0 && (stride * bytes) % 16 == 0);
+// The alignment, in bytes up to 16, of rows at p that are `stride` elements of
+// `bytes` apart and `hidden` long (NULL: not used).
+inline int rows_alignment(const void *p, int64_t stride, int hidden, int bytes) {
+  if (!p) return 16;
+  const uint64_t v = (uint64_t)(uintptr_t)p | (uint64_t)(stride * bytes) | (uint64_t)hidden * bytes | 16;
+  return (int)(v & (~v + 1));
 }
+// f(integral_constant of kWhole, kHalves or kElems) for an alignment in bytes;
+// MIXED: pairs of types, which have no halves.
+template <bool MIXED = false, typename F>
+int by_align(int align, F &&f) {
+  if (align == 16) return f(std::integral_constant<int, kWhole>{});
+  if constexpr (!MIXED)
+    if (align == 8) return f(std::integral_constant<int, kHalves>{});
+  return f(std::integral_constant<int, kElems>{});
+}
+
 // Whether p is aligned to its elements.
 inline bool elem_aligned(const void *p, int bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
 

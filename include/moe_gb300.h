@@ -81,7 +81,8 @@ extern "C" {
 #define MOE_MAX_ROWS_TC 4096      /* M the layer admits on the tensor-core path
                                      (prefill-sized batches of FP8 experts)     */
 
-#define MOE_MAX_NORM_HIDDEN 16384 /* hidden the RMS norm admits                 */
+#define MOE_MAX_ROW_HIDDEN 16384 /* hidden of token and expert rows (dispatch,
+                                    combine, RMS norm and their gradients)     */
 
 /* One projection of all experts of a set.  Layout for `rows` x `cols`
  * (gate/up: rows = inter, cols = hidden; down: rows = hidden, cols = inter),
@@ -444,16 +445,17 @@ int moe_decode_layer_noalloc(const moe_layer_desc *layer, const uint16_t *x, int
  *    below the total (num_tokens_post_padded) are set to zero, so that a
  *    grouped product over whole blocks reads no garbage; rows at or past the
  *    total stay as they were.  Padding rows of inputs are never read.
- *  - M = 0 is valid.  1 <= top_k <= 32, M * top_k <= MOE_MAX_SLOTS, any
- *    hidden >= 1: rows that are whole 16-byte pieces (16-byte aligned, hidden a
- *    multiple of 8) take the fast path, others are served element by element.
+ *  - M = 0 is valid.  1 <= top_k <= 32, M * top_k <= MOE_MAX_SLOTS, any hidden
+ *    from 1 to MOE_MAX_ROW_HIDDEN: rows that are whole 16-byte pieces (16-byte
+ *    aligned, hidden a multiple of 8) take the fast path, others are served
+ *    element by element.
  *  - A *_stride is the distance of the rows of an input in elements, >= 0 (0:
  *    one row for all).  Outputs and expert-order buffers are dense, and
  *    overlap no input unless stated.
  *  - Results are bit-deterministic, and a row's bits do not depend on M.
  *  - Errors: MOE_EINVAL (NULL, negative sizes or strides, unknown type, a
- *    pointer not aligned to its elements), MOE_EUNSUPPORTED (top_k, M * top_k,
- *    or a pair of types that is not listed). */
+ *    pointer not aligned to its elements), MOE_EUNSUPPORTED (hidden, top_k,
+ *    M * top_k, or a pair of types that is not listed). */
 
 /* Token rows into expert order ("fp8_moe_grouped.rs": the sorted rows that the
  * grouped launchers of moe_fp8_grouped_sort's tables work on):
@@ -541,7 +543,7 @@ int moe_topk_softmax_backward(const int32_t *topk_ids, const float *topk_w,
  *   [M][ceil(hidden/128)] float (both or neither); rstd [M] float.  Every
  *   output may be NULL, not all of them.  sum_out or out may be x's or
  *   residual's own buffer when that input is dense (stride = hidden).
- * M = 0 is valid; any hidden from 1 to MOE_MAX_NORM_HIDDEN, whole 16-byte
+ * M = 0 is valid; any hidden from 1 to MOE_MAX_ROW_HIDDEN, whole 16-byte
  * pieces fast as above; a row's bits do not depend on M.
  * Errors: MOE_EINVAL (NULL, sizes, strides, eps negative or not finite, one of
  * codes and scale alone, a strided input shared with an output, misaligned),
@@ -589,7 +591,7 @@ int moe_add_rmsnorm_backward(const void *dout, int64_t dout_stride,
  *   bits, dense; normed and out aligned as moe_decode_layer's x and out.
  *   sum_out may be residual's or x's buffer; sum_out, normed and out are three
  *   different buffers.  Workspace rules and shape admission are
- *   moe_decode_layer's (hidden up to MOE_MAX_NORM_HIDDEN).
+ *   moe_decode_layer's (hidden up to MOE_MAX_ROW_HIDDEN).
  * Errors: as the two calls; nothing is launched then. */
 int moe_decode_block(const moe_layer_desc *layer, const uint16_t *x,
                      const uint16_t *residual, const uint16_t *norm_weight,

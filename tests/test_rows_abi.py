@@ -62,16 +62,16 @@ REFUSED = [
         dict(rows=ODD), dict(x_scale=F), dict(rows_scale=F), dict(dtype=E4),
         dict(dtype=E4, x_scale=F), dict(dtype=E4, rows_scale=F),
         dict(dtype=E4, x_scale=ODD, rows_scale=F)]),
-    ("moe_dispatch", DISPATCH, EUNS, [dict(top_k=33), dict(M=1 << 20)]),
+    ("moe_dispatch", DISPATCH, EUNS, [dict(hidden=16385), dict(top_k=33), dict(M=1 << 20)]),
     ("moe_dispatch_backward", DISPATCH_BWD, EINVAL, [
         dict(drows=None), dict(dx=None), dict(token_to_perm=None), dict(dtype=E4), dict(dtype=0),
         dict(M=-1), dict(drows=ODD), dict(dx=ODD), dict(hidden=0), dict(top_k=0)]),
-    ("moe_dispatch_backward", DISPATCH_BWD, EUNS, [dict(top_k=33), dict(M=1 << 20)]),
+    ("moe_dispatch_backward", DISPATCH_BWD, EUNS, [dict(hidden=16385), dict(top_k=33), dict(M=1 << 20)]),
     ("moe_combine", COMBINE, EINVAL, [
         dict(rows=None), dict(out=None), dict(topk_w=None), dict(token_to_perm=None),
         dict(rows_dtype=E4), dict(out_dtype=0), dict(M=-1), dict(rows=ODD), dict(out=ODD)]),
     ("moe_combine", COMBINE, EUNS, [
-        dict(out_dtype=HF), dict(out_dtype=FL), dict(rows_dtype=HF), dict(top_k=33),
+        dict(hidden=16385), dict(out_dtype=HF), dict(out_dtype=FL), dict(rows_dtype=HF), dict(top_k=33),
         dict(M=1 << 20)]),
     ("moe_combine_backward", COMBINE_BWD, EINVAL, [
         dict(dout=None), dict(rows=None), dict(topk_w=None), dict(token_to_perm=None),
@@ -79,7 +79,7 @@ REFUSED = [
         dict(drows=None, dtopk_w=None), dict(dout=ODD), dict(rows=ODD), dict(drows=ODD),
         dict(rows_dtype=E4), dict(out_dtype=E4), dict(M=-1), dict(hidden=0)]),
     ("moe_combine_backward", COMBINE_BWD, EUNS, [
-        dict(out_dtype=HF), dict(rows_dtype=HF), dict(top_k=33), dict(M=1 << 20)]),
+        dict(hidden=16385), dict(out_dtype=HF), dict(rows_dtype=HF), dict(top_k=33), dict(M=1 << 20)]),
     ("moe_topk_softmax_backward", TOPK_BWD, EINVAL, [
         dict(topk_ids=None), dict(topk_w=None), dict(dtopk_w=None), dict(dlogits=None), dict(M=-1),
         dict(top_k=0), dict(top_k=9), dict(num_experts=0), dict(dlogits=ODD), dict(topk_ids=ODD)]),

@@ -100,7 +100,9 @@ def padding(t, n):
 SHAPES = [(1, 128, 8, 2, 16, 0.0), (8, 2048, 128, 8, 16, 0.0), (3, 1, 4, 1, 1, 0.0),
           (37, 999, 16, 3, 8, 0.4), (128, 4096, 256, 8, 64, 0.0), (65, 264, 64, 32, 16, 0.2),
           (1000, 520, 24, 6, 128, 0.5), (2, 8192, 8, 8, 64, 0.0), (300, 12, 1024, 10, 4, 0.9),
-          (17, 2050, 4, 4, 64, 1.0)]
+          (17, 2050, 4, 4, 64, 1.0), (5, 16384, 8, 3, 16, 0.0), (700, 72, 16, 1, 16, 0.3),
+          (90, 10007, 8, 2, 32, 0.0), (2500, 1024, 64, 8, 16, 0.2),
+          (40, 1540, 8, 3, 16, 0.2), (1100, 100, 8, 5, 4, 0.0)]
 
 
 def _shape_id(v):
@@ -433,7 +435,7 @@ def test_topk_softmax_gradient_of_repeated_and_missing_ids():
 # --------------------------------------------------------------------------
 
 NORM_SHAPES = [(1, 1), (3, 7), (5, 64), (2, 128), (9, 200), (4, 257), (8, 2048), (33, 2880),
-               (3, 4096), (2, 5001), (7, 8192), (2, 12345), (2, 16384), (600, 256)]
+               (3, 4096), (2, 5001), (7, 8192), (2, 12345), (2, 16384), (600, 256), (6, 2884), (400, 513)]
 TYPES = [(BF, BF), (BF, FL), (HF, HF), (HF, FL), (FL, FL)]
 norm_shapes = pytest.mark.parametrize("M,H", NORM_SHAPES)
 types = pytest.mark.parametrize("dt,wt", TYPES, ids=_shape_id)
