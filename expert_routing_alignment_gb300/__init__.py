@@ -526,15 +526,15 @@ def _row_stride(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) ->
                      f"got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
 
 
-def _empty(shape: tuple, dtype: torch.dtype, dev: int, stream) -> torch.Tensor:
+def _empty(shape: tuple, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
     """A new output: it belongs to the stream that the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else \
             torch.cuda.default_stream()
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _table(name: str, t: torch.Tensor, least: int) -> int:
@@ -585,10 +585,10 @@ def moe_dispatch(x: torch.Tensor, tables: dict, top_k: int, rows: Optional[torch
             rs_at = _at("rows_scale", rows_scale, torch.float32, (n_rows, blocks))
     dev = _on_device(x, ttp, sti, total, rows, x_scale, rows_scale, err_word)
     if r_at is None:
-        rows = _empty((n_rows, H), dtype, dev, stream)
+        rows = _empty((n_rows, H), dtype, x.device, stream)
         r_at = rows.data_ptr()
     if xs_at is not None and rs_at is None:
-        rows_scale = _empty((n_rows, blocks), torch.float32, dev, stream)
+        rows_scale = _empty((n_rows, blocks), torch.float32, x.device, stream)
         rs_at = rows_scale.data_ptr()
     _check("moe_dispatch", load().moe_dispatch(
         x.data_ptr(), xs, xs_at, kind, M, top_k, H, t_at, s_at, n_at, n_rows, r_at, rs_at, e_at,
@@ -608,7 +608,7 @@ def moe_dispatch_backward(drows: torch.Tensor, tables: dict, M: int, top_k: int,
     x_at = None if dx is None else _at("dx", dx, dtype, (M, H))
     dev = _on_device(drows, ttp, dx, err_word)
     if x_at is None:
-        dx = _empty((M, H), dtype, dev, stream)
+        dx = _empty((M, H), dtype, drows.device, stream)
         x_at = dx.data_ptr()
     _check("moe_dispatch_backward", load().moe_dispatch_backward(
         r_at, kind, M, top_k, H, t_at, n_rows, x_at, e_at, _handle(stream, dev)))
@@ -633,7 +633,7 @@ def moe_combine(rows: torch.Tensor, topk_w: torch.Tensor, tables: dict,
     o_at = None if out is None else _at("out", out, otype, (M, H))
     dev = _on_device(rows, topk_w, ttp, out, err_word)
     if o_at is None:
-        out = _empty((M, H), otype, dev, stream)
+        out = _empty((M, H), otype, rows.device, stream)
         o_at = out.data_ptr()
     _check("moe_combine", load().moe_combine(
         r_at, kind, w_at, t_at, M, k, H, n_rows, okind, o_at, e_at, _handle(stream, dev)))
@@ -678,10 +678,10 @@ def moe_combine_backward(dout: torch.Tensor, rows: Optional[torch.Tensor], topk_
     dw_at = None if dtopk_w is None else _at("dtopk_w", dtopk_w, torch.float32, (M, k))
     dev = _on_device(dout, rows, topk_w, ttp, sti, total, drows, dtopk_w, err_word)
     if want_drows and dr_at is None:
-        drows = _empty((n_rows, H), rtype, dev, stream)
+        drows = _empty((n_rows, H), rtype, dout.device, stream)
         dr_at = drows.data_ptr()
     if want_dtopk_w and dw_at is None:
-        dtopk_w = _empty((M, k), torch.float32, dev, stream)
+        dtopk_w = _empty((M, k), torch.float32, dout.device, stream)
         dw_at = dtopk_w.data_ptr()
     _check("moe_combine_backward", load().moe_combine_backward(
         dout.data_ptr(), ds, okind, r_at, rkind, w_at, t_at, s_at, n_at, M, k, H, n_rows, dr_at,
@@ -704,7 +704,7 @@ def moe_topk_softmax_backward(topk_ids: torch.Tensor, topk_w: torch.Tensor,
     e_at = _err(err_word)
     dev = _on_device(topk_ids, topk_w, dtopk_w, dlogits, err_word)
     if l_at is None:
-        dlogits = _empty((M, num_experts), torch.float32, dev, stream)
+        dlogits = _empty((M, num_experts), torch.float32, topk_w.device, stream)
         l_at = dlogits.data_ptr()
     _check("moe_topk_softmax_backward", load().moe_topk_softmax_backward(
         i_at, w_at, d_at, M, num_experts, k, l_at, e_at, _handle(stream, dev)))
@@ -728,8 +728,8 @@ def alloc_add_rmsnorm_outputs(x: torch.Tensor, want: Sequence[str], stream=None)
     """Buffers for moe_add_rmsnorm: "out", "sum" [M, H] of x's type, "codes"
     float8_e4m3fn [M, H] and "scale" fp32 [M, ceil(H / 128)], "rstd" fp32 [M]."""
     M, H = x.shape
-    dev = _on_device(x)
-    return {name: _empty(*_norm_output(name, x.dtype, M, H), dev, stream) for name in want}
+    device = x.device
+    return {name: _empty(*_norm_output(name, x.dtype, M, H), device, stream) for name in want}
 
 
 def moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -756,7 +756,8 @@ def moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
         dev = _on_device(x, weight, residual, *out.values())
     else:
         dev = _on_device(x, weight, residual)
-        out = {name: _empty(*_norm_output(name, dtype, M, H), dev, stream) for name in want}
+        device = x.device
+        out = {name: _empty(*_norm_output(name, dtype, M, H), device, stream) for name in want}
         at = {name: t.data_ptr() for name, t in out.items()}
     get = at.get
     _check("moe_add_rmsnorm", load().moe_add_rmsnorm(
@@ -802,14 +803,14 @@ def moe_add_rmsnorm_backward(dout: torch.Tensor, sum: torch.Tensor, weight: torc
             ws_at, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     dev = _on_device(dout, sum, weight, rstd, dsum, dx, dweight, workspace)
     if x_at is None:
-        dx = _empty((M, H), dtype, dev, stream)
+        dx = _empty((M, H), dtype, dout.device, stream)
         x_at = dx.data_ptr()
     if want_dweight and g_at is None:
-        dweight = _empty((H,), torch.float32, dev, stream)
+        dweight = _empty((H,), torch.float32, dout.device, stream)
         g_at = dweight.data_ptr()
     if want_dweight and workspace is None:
         nbytes = add_rmsnorm_backward_workspace_bytes(M, H)
-        workspace = _empty((nbytes,), torch.uint8, dev, stream)
+        workspace = _empty((nbytes,), torch.uint8, dout.device, stream)
         ws_at = workspace.data_ptr()
     _check("moe_add_rmsnorm_backward", load().moe_add_rmsnorm_backward(
         dout.data_ptr(), ds, sum.data_ptr(), ss, w_at, r_at, d_at, es, kind, wkind, M, H, x_at,
@@ -836,10 +837,10 @@ def moe_decode_block(layer: LayerDesc, x: torch.Tensor, residual: Optional[torch
     w_at, e_at = _at("norm_weight", norm_weight, bf16, (H,)), _err(err_word)
     dev = _on_device(x, residual, norm_weight, out, workspace, sum_out, normed, err_word)
     if s_at is None:
-        sum_out = _empty((M, H), bf16, dev, stream)
+        sum_out = _empty((M, H), bf16, x.device, stream)
         s_at = sum_out.data_ptr()
     if n_at is None:
-        normed = _empty((M, H), bf16, dev, stream)
+        normed = _empty((M, H), bf16, x.device, stream)
         n_at = normed.data_ptr()
     _check("moe_decode_block", load().moe_decode_block(
         ctypes.pointer(layer._struct), x_at, r_at, w_at, eps, M, s_at, n_at, o_at,

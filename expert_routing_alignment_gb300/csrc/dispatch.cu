@@ -342,10 +342,10 @@ template <typename R, typename O, bool WEIGHTED>
 int launch_combine(const SlotArgs &a, const void *rows, const float *w, int H, void *out, int align,
                    void *stream) {
   const Parts s = split_parts((H + kPer16<R> - 1) / kPer16<R>);
-  // Up to eight tokens and 32 slots a CTA while eight CTAs an SM remain: at
-  // M = 4000, top_k = 6, hidden = 2880 with three of four slots skipped 23.4 us
-  // with one token a CTA and 13.9 with five; at top_k = 8 with none skipped
-  // (M = 4096, hidden = 7168) 98.7 and 85.3.
+  // Up to eight tokens and 32 slots a CTA while eight CTAs an SM remain: bf16
+  // at M = 4000, top_k = 6, hidden = 2880 with three of four slots skipped
+  // 23.4 us with one token a CTA and 13.9 with five; at M = 4096, top_k = 8,
+  // hidden = 7168 with none skipped 87.2 with one and 85.2 with four.
   const int64_t room = (int64_t)a.M * s.parts / (8 * sm_count());
   const int fit = 32 / a.k < 8 ? 32 / a.k : 8;
   const int tok = room < 1 ? 1 : room < fit ? (int)room : fit;
@@ -382,8 +382,10 @@ int launch_combine_grad(const SlotArgs &a, const void *dout, int64_t stride, con
 template <typename R, typename O, bool DW, bool DR>
 int launch_combine_grad(const SlotArgs &a, const void *dout, int64_t stride, const void *rows,
                         const float *w, int H, void *drows, float *dw, int align, void *stream) {
-  // Eight slots a CTA in flight when there are tokens enough: at M = 16384,
-  // top_k = 1, hidden = 1024 44.6 us with one token a CTA and 22.3 with four.
+  // Eight slots a CTA in flight when there are tokens enough: bf16 at
+  // M = 16384, top_k = 1, hidden = 1024 44.6 us with one token a CTA and 22.3
+  // with four; at M = 8192, top_k = 4, hidden = 2048 with half of the slots
+  // skipped 57.0 with one and 41.4 with two.
   const int tok = a.M < 1024 || a.k > 4 ? 1 : a.k > 2 ? 2 : 4;
   auto go = [&](auto t) {
     return launch_combine_grad<R, O, decltype(t)::value, DW, DR>(a, dout, stride, rows, w, H, drows,
@@ -460,7 +462,8 @@ int combine(const void *rows, int rows_dtype, const float *topk_w, const int32_t
     using OT = decltype(O);
     // without weights (the gradient of the dispatch) both types are one
     if constexpr (std::is_same_v<RT, OT>)
-      if (!topk_w) return launch_combine<RT, OT, false>(a, rows, topk_w, hidden, out, align, stream);
+      if (!topk_w)
+        return launch_combine<RT, OT, false>(a, rows, topk_w, hidden, out, align, stream);
     return launch_combine<RT, OT, true>(a, rows, topk_w, hidden, out, align, stream);
   });
 }
@@ -493,12 +496,11 @@ extern "C" int moe_dispatch(const void *x, int64_t x_stride, const float *x_scal
   int align = rows_alignment(x, x_stride, hidden, eb);
   if (const int k = rows_alignment(rows, hidden, hidden, eb); k < align) align = k;
   const Parts s = split_parts((len + 15) / 16);
-  // two tokens a CTA at least when there are many (M = 4000, top_k = 6: 16.0 us
-  // with one, 12.9 with two), more with fewer slots (M = 16384, top_k = 1: 18.5
-  // and, with eight, 13.0)
-  const int most = kMaxK / top_k;
-  int tok = M < 1024 ? 1 : top_k == 1 ? 8 : top_k == 2 ? 4 : 2;
-  if (tok > most) tok = most;
+  // Two tokens a CTA when there are many of few slots: bf16 at M = 16384,
+  // top_k = 1, hidden = 1024 19.2 us with one and 13.2 with two (13.0 with
+  // eight); at M = 4000, top_k = 6, hidden = 2880 16.0 and 12.1; at top_k = 8
+  // (M = 4096, hidden = 7168) 103.7 and 104.3.
+  const int tok = M < 1024 || top_k > 6 ? 1 : 2;
   const dim3 grid((unsigned)pad_ctas(ceil_div64(M, tok), num_rows), s.parts), block(s.threads);
   auto launch = [&](auto kernel) {
     return launch_pdl(kernel, grid, block, 0, stream, a, static_cast<const char *>(x),
@@ -506,10 +508,7 @@ extern "C" int moe_dispatch(const void *x, int64_t x_stride, const float *x_scal
   };
   auto go = [&](auto es, auto al) {
     constexpr int ES = decltype(es)::value, A = decltype(al)::value;
-    if (tok == 8) return launch(dispatch_kernel<ES, 8, A>);
-    if (tok == 4) return launch(dispatch_kernel<ES, 4, A>);
-    if (tok == 2) return launch(dispatch_kernel<ES, 2, A>);
-    return launch(dispatch_kernel<ES, 1, A>);
+    return tok == 2 ? launch(dispatch_kernel<ES, 2, A>) : launch(dispatch_kernel<ES, 1, A>);
   };
   // by pieces and halves every type is the same
   return by_align(align, [&](auto al) {

@@ -37,7 +37,7 @@ __device__ __forceinline__ uint16_t to_e4m3x2(float lo, float hi) {
 // butterfly in the warp, then the warps' sums four by four.  One barrier, of
 // the group alone; calls that follow one another take turns between two
 // `red`s, whose unused places are zero.
-constexpr int kRedFloats = 64;   // a multiple of four per group, 48 at most (12 groups of two warps)
+constexpr int kRedFloats = 64;   // a multiple of four per group, 48 at most (12 of two warps)
 __device__ __forceinline__ float group_sum(float v, float *red) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
@@ -219,7 +219,8 @@ __device__ __forceinline__ f32x2 code_quotient(f32x2 p, f32x2 minus_m, f32x2 y) 
 }
 
 template <typename T, typename W, int CH, int A>
-__global__ void __launch_bounds__(CH <= 2 ? 448 : 512, CH <= 2 ? 2 : 1) add_rmsnorm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(CH <= 2 ? 448 : 512, CH <= 2 ? 2 : 1)
+    add_rmsnorm_kernel(NormArgs a) {
   using TB = typename T::bits;
   using WB = typename W::bits;
   constexpr int N = kPer16<T>;
@@ -425,7 +426,8 @@ __global__ void __launch_bounds__(grad_threads(CH)) rmsnorm_grad_kernel(NormGrad
 #pragma unroll
       for (int e = 0; e < N / 2; ++e)
         v[e] = fma2(s[e], pair(back, back), fma2(rstd2, mul2(d[e], wf[e]), v[e]));
-      raw_store<T, N, A>(static_cast<TB *>(a.dx) + out_at, tid + i * tpr, H, raw_down<T>(v), feed.on(i));
+      raw_store<T, N, A>(static_cast<TB *>(a.dx) + out_at, tid + i * tpr, H, raw_down<T>(v),
+                         feed.on(i));
     }
     // the slots of this row have been read: the row `depth` turns on goes there
     feed.start(row + a.depth * step, row + a.depth * step < a.M);
@@ -540,6 +542,7 @@ int check_add_rmsnorm(const void *x, int64_t x_stride, const void *residual,
       !elem_aligned(out, b) || !elem_aligned(weight, dtype_bytes(weight_dtype)) ||
       !elem_aligned(out_scale, 4) || !elem_aligned(rstd, 4))
     return MOE_EINVAL;
+  if (sum_out && sum_out == out) return MOE_EINVAL;
   // an output may take an input's place only element for element
   if ((x_stride != hidden && (x == sum_out || x == out)) ||
       (residual && residual_stride != hidden && (residual == sum_out || residual == out)))

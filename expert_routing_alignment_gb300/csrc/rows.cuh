@@ -362,7 +362,9 @@ __device__ __forceinline__ Raw<T, kPer16<T>> raw_load_shared(uint32_t shared) {
                : "memory");
   return r;
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
 // Until at most depth - 1 of this thread's committed groups are in flight.
 __device__ __forceinline__ void copies_wait(int depth) {
   if (depth >= 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
@@ -387,7 +389,8 @@ inline int dtype_bytes(int dtype) {
 // `bytes` apart and `hidden` long (NULL: not used).
 inline int rows_alignment(const void *p, int64_t stride, int hidden, int bytes) {
   if (!p) return 16;
-  const uint64_t v = (uint64_t)(uintptr_t)p | (uint64_t)(stride * bytes) | (uint64_t)hidden * bytes | 16;
+  const uint64_t v = (uint64_t)(uintptr_t)p | (uint64_t)(stride * bytes) |
+                     (uint64_t)hidden * bytes | 16;
   return (int)(v & (~v + 1));
 }
 // f(integral_constant of kWhole, kHalves or kElems) for an alignment in bytes;

@@ -541,12 +541,14 @@ int moe_topk_softmax_backward(const int32_t *topk_ids, const float *topk_w,
  *   x, residual: M rows, *_stride apart; weight [hidden]; sum_out, out
  *   [M][hidden]; out_codes [M][hidden] bytes with out_scale
  *   [M][ceil(hidden/128)] float (both or neither); rstd [M] float.  Every
- *   output may be NULL, not all of them.  sum_out or out may be x's or
- *   residual's own buffer when that input is dense (stride = hidden).
+ *   output may be NULL, not all of them.  sum_out and out are different
+ *   buffers; either may be x's or residual's own when that input is dense
+ *   (stride = hidden).
  * M = 0 is valid; any hidden from 1 to MOE_MAX_ROW_HIDDEN, whole 16-byte
  * pieces fast as above; a row's bits do not depend on M.
  * Errors: MOE_EINVAL (NULL, sizes, strides, eps negative or not finite, one of
- * codes and scale alone, a strided input shared with an output, misaligned),
+ * codes and scale alone, sum_out and out the same, a strided input shared with
+ * an output, misaligned),
  * MOE_EUNSUPPORTED (hidden, types). */
 int moe_add_rmsnorm(const void *x, int64_t x_stride, const void *residual,
                     int64_t residual_stride, const void *weight, int dtype,

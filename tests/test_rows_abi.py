@@ -47,8 +47,9 @@ COMBINE_BWD = dict(dout=F, dout_stride=256, out_dtype=BF, rows=F, rows_dtype=BF,
                    hidden=256, num_rows=64, drows=F, dtopk_w=F, err_word=None, stream=None)
 TOPK_BWD = dict(topk_ids=F, topk_w=F, dtopk_w=F, M=4, num_experts=8, top_k=2, dlogits=F,
                 err_word=None, stream=None)
+F2 = ctypes.c_void_p(8192)
 NORM = dict(x=F, x_stride=256, residual=F, residual_stride=256, weight=F, dtype=BF,
-            weight_dtype=BF, M=4, hidden=256, eps=1e-6, sum_out=F, out=F, out_codes=F,
+            weight_dtype=BF, M=4, hidden=256, eps=1e-6, sum_out=F, out=F2, out_codes=F,
             out_scale=F, rstd=F, stream=None)
 NORM_BWD = dict(dout=F, dout_stride=256, sum=F, sum_stride=256, weight=F, rstd=F, dsum=F,
                 dsum_stride=256, dtype=BF, weight_dtype=BF, M=4, hidden=256, dx=F, dweight=F,
@@ -66,12 +67,14 @@ REFUSED = [
     ("moe_dispatch_backward", DISPATCH_BWD, EINVAL, [
         dict(drows=None), dict(dx=None), dict(token_to_perm=None), dict(dtype=E4), dict(dtype=0),
         dict(M=-1), dict(drows=ODD), dict(dx=ODD), dict(hidden=0), dict(top_k=0)]),
-    ("moe_dispatch_backward", DISPATCH_BWD, EUNS, [dict(hidden=16385), dict(top_k=33), dict(M=1 << 20)]),
+    ("moe_dispatch_backward", DISPATCH_BWD, EUNS, [
+        dict(hidden=16385), dict(top_k=33), dict(M=1 << 20)]),
     ("moe_combine", COMBINE, EINVAL, [
         dict(rows=None), dict(out=None), dict(topk_w=None), dict(token_to_perm=None),
         dict(rows_dtype=E4), dict(out_dtype=0), dict(M=-1), dict(rows=ODD), dict(out=ODD)]),
     ("moe_combine", COMBINE, EUNS, [
-        dict(hidden=16385), dict(out_dtype=HF), dict(out_dtype=FL), dict(rows_dtype=HF), dict(top_k=33),
+        dict(hidden=16385), dict(out_dtype=HF), dict(out_dtype=FL), dict(rows_dtype=HF),
+        dict(top_k=33),
         dict(M=1 << 20)]),
     ("moe_combine_backward", COMBINE_BWD, EINVAL, [
         dict(dout=None), dict(rows=None), dict(topk_w=None), dict(token_to_perm=None),
@@ -79,7 +82,8 @@ REFUSED = [
         dict(drows=None, dtopk_w=None), dict(dout=ODD), dict(rows=ODD), dict(drows=ODD),
         dict(rows_dtype=E4), dict(out_dtype=E4), dict(M=-1), dict(hidden=0)]),
     ("moe_combine_backward", COMBINE_BWD, EUNS, [
-        dict(hidden=16385), dict(out_dtype=HF), dict(rows_dtype=HF), dict(top_k=33), dict(M=1 << 20)]),
+        dict(hidden=16385), dict(out_dtype=HF), dict(rows_dtype=HF), dict(top_k=33),
+        dict(M=1 << 20)]),
     ("moe_topk_softmax_backward", TOPK_BWD, EINVAL, [
         dict(topk_ids=None), dict(topk_w=None), dict(dtopk_w=None), dict(dlogits=None), dict(M=-1),
         dict(top_k=0), dict(top_k=9), dict(num_experts=0), dict(dlogits=ODD), dict(topk_ids=ODD)]),
@@ -91,6 +95,7 @@ REFUSED = [
         dict(eps=float("nan")), dict(eps=float("inf")), dict(out_scale=None), dict(out_codes=None),
         dict(sum_out=None, out=None, out_codes=None, out_scale=None, rstd=None), dict(x=ODD),
         dict(residual=ODD), dict(weight=ODD), dict(rstd=ODD), dict(out_scale=ODD),
+        dict(out=F),   # the same as sum_out
         dict(x_stride=512), dict(residual_stride=0)]),   # strided, and sum_out == x == residual
     ("moe_add_rmsnorm", NORM, EUNS, [
         dict(hidden=16385), dict(weight_dtype=HF), dict(dtype=FL, weight_dtype=BF)]),

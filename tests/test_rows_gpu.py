@@ -16,6 +16,7 @@ finfo(T).eps / 2 the rounding to T; tiny(T) half of T's smallest subnormal):
 from __future__ import annotations
 
 import math
+import os
 
 import pytest
 import torch
@@ -102,7 +103,9 @@ SHAPES = [(1, 128, 8, 2, 16, 0.0), (8, 2048, 128, 8, 16, 0.0), (3, 1, 4, 1, 1, 0
           (1000, 520, 24, 6, 128, 0.5), (2, 8192, 8, 8, 64, 0.0), (300, 12, 1024, 10, 4, 0.9),
           (17, 2050, 4, 4, 64, 1.0), (5, 16384, 8, 3, 16, 0.0), (700, 72, 16, 1, 16, 0.3),
           (90, 10007, 8, 2, 32, 0.0), (2500, 1024, 64, 8, 16, 0.2),
-          (40, 1540, 8, 3, 16, 0.2), (1100, 100, 8, 5, 4, 0.0)]
+          (40, 1540, 8, 3, 16, 0.2), (1100, 100, 8, 5, 4, 0.0), (1030, 77, 8, 2, 16, 0.3),
+          (1200, 264, 8, 4, 8, 0.5), (1101, 33, 64, 32, 4, 0.0), (1500, 48, 8, 1, 16, 0.0),
+          (1027, 131, 8, 7, 16, 0.9)]
 
 
 def _shape_id(v):
@@ -167,6 +170,44 @@ def test_dispatch_gradient(shape, dtype):
     assert dx.dtype == dtype
     close(dx, v.sum(1), v.abs().sum(1), k * U)
     assert not dx[(perm < 0).all(1)].any()
+
+
+@pytest.mark.parametrize("H,shift", [(264, 0), (264, 4), (1028, 0), (999, 0), (999, 3), (17, 1),
+                                     (1, 0), (8, 5), (2051, 7)])
+@pytest.mark.parametrize("dtype", [BF, FL], ids=_shape_id)
+def test_nothing_outside_the_outputs_is_written(H, shift, dtype):
+    """Outputs inside larger buffers, at every kind of alignment, with guards
+    on both sides; the same bits as in buffers of their own."""
+    M, k, E = 13, 3, 4
+    _, w, t = route(M, E, k, 8, 130)
+    n = t["max_total"]
+    g = gen(131)
+    x, r, dout = (randn(g, M, H, dtype=dtype) for _ in range(3))
+    rows, weight = randn(g, n, H, dtype=dtype), randn(g, H, dtype=dtype)
+    made = []
+
+    def guarded(count):
+        buf = torch.full((count * H + 64,), 77.0, dtype=dtype, device="cuda")
+        made.append((buf, count))
+        return buf[32 + shift: 32 + shift + count * H].view(count, H)
+    total = int(t["num_tokens_post_padded"])
+    a = moe.moe_dispatch(x, t, k, rows=guarded(n))[:total]
+    b = moe.moe_dispatch(x, t, k)[:total]
+    pairs_ = [(a, b), (moe.moe_dispatch_backward(rows, t, M, k, dx=guarded(M)),
+                       moe.moe_dispatch_backward(rows, t, M, k)),
+              (moe.moe_combine(rows, w, t, out=guarded(M)), moe.moe_combine(rows, w, t)),
+              (moe.moe_combine_backward(dout, rows, w, t, drows=guarded(n))[0][:total],
+               moe.moe_combine_backward(dout, rows, w, t)[0][:total])]
+    o = moe.moe_add_rmsnorm(x, weight, residual=r, want=("out", "sum", "rstd"))
+    p = moe.moe_add_rmsnorm(x, weight, residual=r, out=dict(out=guarded(M), sum=guarded(M)))
+    pairs_ += [(p["out"], o["out"]), (p["sum"], o["sum"]),
+               (moe.moe_add_rmsnorm_backward(dout, r, weight, o["rstd"], dsum=x, dx=guarded(M))[0],
+                moe.moe_add_rmsnorm_backward(dout, r, weight, o["rstd"], dsum=x)[0])]
+    torch.cuda.synchronize()
+    for i, (got, want) in enumerate(pairs_):
+        assert torch.equal(bits(got), bits(want)), i
+    for i, (buf, count) in enumerate(made):
+        assert (buf[: 32 + shift] == 77.0).all() and (buf[32 + shift + count * H:] == 77.0).all(), i
 
 
 @pytest.mark.parametrize("H,start,width", [(256, 8, 512), (256, 1, 400), (100, 4, 104),
@@ -435,7 +476,8 @@ def test_topk_softmax_gradient_of_repeated_and_missing_ids():
 # --------------------------------------------------------------------------
 
 NORM_SHAPES = [(1, 1), (3, 7), (5, 64), (2, 128), (9, 200), (4, 257), (8, 2048), (33, 2880),
-               (3, 4096), (2, 5001), (7, 8192), (2, 12345), (2, 16384), (600, 256), (6, 2884), (400, 513)]
+               (3, 4096), (2, 5001), (7, 8192), (2, 12345), (2, 16384), (600, 256), (6, 2884),
+               (400, 513)]
 TYPES = [(BF, BF), (BF, FL), (HF, HF), (HF, FL), (FL, FL)]
 norm_shapes = pytest.mark.parametrize("M,H", NORM_SHAPES)
 types = pytest.mark.parametrize("dt,wt", TYPES, ids=_shape_id)
@@ -538,6 +580,29 @@ def test_norm_of_rows_without_size_and_of_extremes():
     tiny_row = torch.full((1, H), 2.0 ** -126, dtype=FL, device="cuda")
     o = moe.moe_add_rmsnorm(tiny_row, torch.ones(H, device="cuda"), 1.0, want=("codes", "scale"))
     assert (o["scale"] == 2.0 ** -126).all() and (o["codes"].float() == 1).all()
+
+
+@pytest.mark.parametrize("dtype,lo,hi", [(BF, -0x7F80, 0x7F80), (HF, -0x7C00, 0x7C00)],
+                         ids=["bfloat16", "float16"])
+def test_sums_of_any_two_finite_values(dtype, lo, hi):
+    """Random finite bit patterns, subnormal ones and near overflow among them:
+    the stored sum is the exact sum rounded once."""
+    g = gen(140)
+    M, H = 64, 1024
+
+    def any_finite():
+        m = torch.randint(0, hi, (M, H), generator=g, device="cuda")
+        sign = torch.randint(0, 2, (M, H), generator=g, device="cuda") << 15
+        return (m | sign).to(torch.int32).to(torch.int16).view(dtype)
+    x, r = any_finite(), any_finite()
+    x[0, :512] = (torch.randint(0, 128, (512,), generator=g, device="cuda")).to(
+        torch.int16).view(dtype)   # subnormal + subnormal
+    r[0, :512] = x[0, :512].flip(0)
+    w = torch.ones(H, dtype=dtype, device="cuda")
+    s = moe.moe_add_rmsnorm(x, w, residual=r, want=("sum",))["sum"]
+    # the fp32 sum of two such values is exact or far from a tie (their bits
+    # would span more than 24), so rounding it once more is rounding once
+    assert torch.equal(bits(s), bits((x.float() + r.float()).to(dtype)))
 
 
 def test_norm_in_place_and_of_strided_rows():
@@ -728,6 +793,45 @@ def test_captured_chain_replays_on_new_inputs():
         torch.cuda.synchronize()
         for name in ref:
             assert torch.equal(bits(got[name]), bits(ref[name])), name
+
+
+def test_first_calls_can_be_captured():
+    """A process whose first calls of these entry points are inside a capture."""
+    code = """
+import torch, expert_routing_alignment_gb300 as moe
+moe.load()
+torch.manual_seed(0)
+M, H, E, k = 40, 4096, 8, 2
+x, d = (torch.randn(M, H, device="cuda").bfloat16() for _ in range(2))
+w = torch.ones(H, device="cuda", dtype=torch.bfloat16)
+ids, tw = moe.moe_topk_softmax(torch.randn(M, E, device="cuda"), k)
+t = moe.moe_align(ids, E, 16)
+nbytes = moe.add_rmsnorm_backward_workspace_bytes(4 * M, H)
+ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+def run():
+    o = moe.moe_add_rmsnorm(x, w, residual=d, want=("out", "sum", "rstd", "codes", "scale"))
+    rows = moe.moe_dispatch(o["out"], t, k)
+    r8, rs = moe.moe_dispatch(o["codes"], t, k, x_scale=o["scale"])
+    out = moe.moe_combine(rows, tw, t)
+    dr, dw = moe.moe_combine_backward(out, rows, tw, t)
+    dx = moe.moe_dispatch_backward(dr, t, M, k)
+    dl = moe.moe_topk_softmax_backward(ids, tw, dw, E)
+    g, gw = moe.moe_add_rmsnorm_backward(dx, o["sum"], w, o["rstd"], workspace=ws)
+    return out, dw, dl, g, gw, o["codes"].view(torch.uint8), o["scale"]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+for a, b in zip(got, run()):
+    assert torch.equal(a, b)
+print("captured")
+"""
+    import subprocess
+    import sys
+    p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert p.returncode == 0 and "captured" in p.stdout, p.stderr[-2000:]
 
 
 def test_calls_on_two_streams_at_once():
