@@ -194,7 +194,9 @@ struct Weights {
 // 22 + 3 for fp16, rounded once), so the only rounding ahead of the code is
 // the quotient's, and the codes do not depend on the order of the sum of
 // squares.  Where the scale would be below 2^-126 it is 2^-126, so that no
-// scale is zero or subnormal.
+// scale is zero or subnormal.  Bound by HBM: bf16 at M = 32768, hidden = 4096
+// (1.07 GB) 167 us, 6.4 TB/s; with E4M3 output at M = 4096 (118 MB) 22.9 us,
+// 5.2 TB/s, of which launch, first loads and the last rows take about 4.
 
 struct NormArgs {
   const void *x, *r, *w;
@@ -343,7 +345,8 @@ __global__ void __launch_bounds__(CH <= 2 ? 448 : 512, CH <= 2 ? 2 : 1)
 // A group walks over its rows with their part of dw in registers; one CTA an
 // SM adds its groups' parts in order, the CTAs' parts go to the workspace
 // [CTAs][H] and a second kernel adds those in a fixed order, so the bits are
-// the same every time.
+// the same every time.  Bound by HBM: bf16 at M = 10007, hidden = 4096 (328 MB)
+// 54.4 us, 6.0 TB/s, of which the second kernel and its launch take about 4.
 
 struct NormGradArgs {
   const void *dout, *sum, *dsum, *w;
