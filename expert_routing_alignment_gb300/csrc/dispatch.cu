@@ -79,25 +79,27 @@ struct Padding {
 // dispatch: rows[token_to_perm[t][j]] = x[t]
 // ---------------------------------------------------------------------------
 //
-// A copy of bytes, so one kernel serves every type (ES: the element's bytes,
-// for rows that are moved element by element).  A CTA takes TOK tokens and, in
+// A copy, so one kernel serves every type (H elements of ES bytes; whole pieces
+// and halves are the same for all, and H then counts bytes).  A CTA takes TOK tokens and, in
 // grid.y, a part of the row, one 16-byte piece a thread.  Bound by the writes:
 // E4M3 rows at M = 4096, hidden = 4096, top_k = 8 over 256 experts (190 MB, 150
-// of it written) 33 us, 5.7 TB/s; a plain fill writes 3.9 TB/s to this HBM, the
+// of it written) 32 us, 5.9 TB/s; a plain fill writes 3.9 TB/s to this HBM, the
 // L2 takes the rest.  Eight tokens (M = 8, hidden = 2048, 3.3 MB with the
 // padding) take 2.8 us, a launch and two round trips.
 
 template <int ES, int TOK, int A>
 __global__ void __launch_bounds__(256) dispatch_kernel(SlotArgs a, const char *x, int64_t x_stride,
-                                                       const float *xs, int len, int scales,
+                                                       const float *xs, int H, int scales,
                                                        char *rows, float *rs) {
   __shared__ int pos[kMaxK];   // TOK * k <= kMaxK
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, at = (blockIdx.y * blockDim.x + tid) * 16;
-  const bool on = at < len;
+  const int tid = threadIdx.x, c = blockIdx.y * blockDim.x + tid;
+  const bool on = in_row<16 / ES, A>(c, H);
   const int64_t t0 = (int64_t)blockIdx.x * TOK;
-  auto put = [&](int64_t p, const uint4 &v) { store16<ES, A>(rows + p * len, at, len, v, on); };
+  auto put = [&](int64_t p, const uint4 &v) {
+    if (on) store16<ES, A>(rows + p * H * ES, c, H, v);
+  };
   Padding padding;
   padding.look(a);
   if (t0 < a.M) {
@@ -105,7 +107,7 @@ __global__ void __launch_bounds__(256) dispatch_kernel(SlotArgs a, const char *x
 #pragma unroll
     for (int i = 0; i < TOK; ++i) {
       v[i] = make_uint4(0, 0, 0, 0);
-      if (on && t0 + i < a.M) v[i] = load16<ES, A>(x + (t0 + i) * x_stride, at, len);
+      if (on && t0 + i < a.M) v[i] = load16<ES, A>(x + (t0 + i) * x_stride, c, H);
     }
     const int n = (int)min((int64_t)TOK, a.M - t0) * a.k;
     if (tid < n) pos[tid] = position(a, t0 * a.k + tid);
@@ -182,20 +184,22 @@ __global__ void __launch_bounds__(256) combine_kernel(SlotArgs a, const typename
   }
   __syncthreads();
   const int c = blockIdx.y * blockDim.x + threadIdx.x;
-  const bool on = c < (H + N - 1) / N;
-  if (A == kWhole && !on) return;   // kElems: whole warps up to the stores
+  // halves keep their idle lanes: fp16 at M = 3000, top_k = 4, hidden = 2884
+  // 19.1 us, and 27.6 when these return here
+  const bool on = in_row<N, A>(c, H);
+  if (A != kHalves && !on) return;
   const int n = count;
   f32x2 acc[N / 2] = {};
   for (int s0 = 0; s0 < n; s0 += kBatch) {
     Raw<R, N> v[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
-      if ((A == kWhole || on) && s0 + u < n && pos[s0 + u] >= 0)
+      if ((A != kHalves || on) && s0 + u < n && pos[s0 + u] >= 0)
         v[u] = raw_load<R, N, A>(rows + (size_t)pos[s0 + u] * H, c, H);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       if (s0 + u >= n) break;
-      if ((A == kWhole || on) && pos[s0 + u] >= 0) {
+      if ((A != kHalves || on) && pos[s0 + u] >= 0) {
         f32x2 f[N / 2];
         raw_up<R, N>(v[u], f);
         const float wj = WEIGHTED ? wt[s0 + u] : 1.f;
@@ -203,7 +207,8 @@ __global__ void __launch_bounds__(256) combine_kernel(SlotArgs a, const typename
         for (int e = 0; e < N / 2; ++e) acc[e] = fma2(pair(wj, wj), f[e], acc[e]);
       }
       if (const int t = ends[s0 + u]; t >= 0) {
-        raw_store<O, N, A>(out + (t0 + t) * H, c, H, raw_down<O>(acc), A == kWhole || on);
+        if (A != kHalves || on)
+          raw_store<O, N, A>(out + (t0 + t) * H, c, H, raw_down<O>(acc));
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) acc[e] = 0;
       }
@@ -224,9 +229,9 @@ __global__ void __launch_bounds__(256) combine_kernel(SlotArgs a, const typename
 // sums), the warps' sums are added in warp order.  A sum's order depends on
 // hidden and the type alone: a token's bits are the same in every batch.
 // Bound by HBM: bf16 at M = 16384, hidden = 4096, top_k = 8 (2.42 GB, half of
-// it written) 372 us, 6.5 TB/s; three CTAs an SM (72 registers), since 96
+// it written) 365 us, 6.6 TB/s; three CTAs an SM (72 registers), since 96
 // registers and two CTAs took 408 us.  Weights alone (fp32 rows, M = 512,
-// hidden = 4096: 71 MB) 13.9 us, 5.1 TB/s, one wave of four CTAs an SM.
+// hidden = 4096: 71 MB) 14 us, 5.1 TB/s, one wave of four CTAs an SM.
 
 template <typename R, typename O, int TOK, bool DW, bool DR, int A>
 __global__ void __launch_bounds__(256, DR ? 3 : TOK > 1 ? 3 : 4) combine_grad_kernel(
@@ -239,7 +244,6 @@ __global__ void __launch_bounds__(256, DR ? 3 : TOK > 1 ? 3 : 4) combine_grad_ke
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
-  const int pieces = (H + N - 1) / N;
   const int64_t t0 = (int64_t)blockIdx.x * TOK;
   Padding padding;
   if (DR) padding.look(a);
@@ -252,14 +256,12 @@ __global__ void __launch_bounds__(256, DR ? 3 : TOK > 1 ? 3 : 4) combine_grad_ke
     __syncthreads();
     for (int j0 = 0; j0 < a.k; j0 += U) {
       float acc[8] = {};   // slot u of token i at i * U + u
-      // kElems: whole warps up to the stores
-      for (int c = tid; (A == kElems ? c - lane : c) < pieces; c += blockDim.x) {
-        const bool on = A != kElems || c < pieces;
+      for (int c = tid; in_row<N, A>(c, H); c += blockDim.x) {
         Raw<O, N> dr[TOK];
         Raw<R, N> v[TOK][U];
 #pragma unroll
         for (int i = 0; i < TOK; ++i)
-          dr[i] = on && (TOK == 1 || t0 + i < a.M)
+          dr[i] = TOK == 1 || t0 + i < a.M
                       ? raw_load<O, N, A>(dout + (t0 + i) * dout_stride, c, H)
                       : raw_zero<O, N>();
         if (DW) {
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(256, DR ? 3 : TOK > 1 ? 3 : 4) combine_grad_ke
 #pragma unroll
             for (int u = 0; u < U; ++u) {
               const int s = i * a.k + j0 + u;
-              if (on && j0 + u < a.k && pos[s] >= 0)
+              if (j0 + u < a.k && pos[s] >= 0)
                 v[i][u] = raw_load<R, N, A>(rows + (size_t)pos[s] * H, c, H);
             }
         }
@@ -285,9 +287,9 @@ __global__ void __launch_bounds__(256, DR ? 3 : TOK > 1 ? 3 : 4) combine_grad_ke
                 const float wj = wt[s];
 #pragma unroll
                 for (int e = 0; e < N; ++e) g[e] = wj * d[e];
-                raw_store<R, N, A>(drows + (size_t)pos[s] * H, c, H, raw_down<R, N>(g), on);
+                raw_store<R, N, A>(drows + (size_t)pos[s] * H, c, H, raw_down<R, N>(g));
               }
-              if (DW && on) {
+              if (DW) {
                 float f[N];
                 raw_up<R, N>(v[i][u], f);
 #pragma unroll
@@ -327,8 +329,8 @@ __global__ void __launch_bounds__(256, DR ? 3 : TOK > 1 ? 3 : 4) combine_grad_ke
   }
   if (DR)
     padding.clear(a, [&](int64_t p) {
-      for (int c = tid; c - lane < pieces; c += blockDim.x)
-        raw_store<R, N, A>(drows + p * H, c, H, raw_zero<R, N>(), c < pieces);
+      for (int c = tid; in_row<N, A>(c, H); c += blockDim.x)
+        raw_store<R, N, A>(drows + p * H, c, H, raw_zero<R, N>());
     });
 }
 
@@ -366,7 +368,7 @@ int launch_combine(const SlotArgs &a, const void *rows, const float *w, int H, v
   auto go = [&](auto kernel) {
     return launch_pdl(kernel, grid, block, 0, stream, a, r, w, H, tok, o);
   };
-  return by_align<!std::is_same_v<R, O>>(align, [&](auto al) {
+  return by_align<!std::is_same_v<R, O>>(align, H, sizeof(typename R::bits), [&](auto al) {
     return go(combine_kernel<R, O, WEIGHTED, decltype(al)::value>);
   });
 }
@@ -385,7 +387,7 @@ int launch_combine_grad(const SlotArgs &a, const void *dout, int64_t stride, con
   auto go = [&](auto kernel) {
     return launch_pdl(kernel, grid, block, 0, stream, a, d, stride, r, w, H, g, dw);
   };
-  return by_align<!std::is_same_v<R, O>>(align, [&](auto al) {
+  return by_align<!std::is_same_v<R, O>>(align, H, sizeof(typename R::bits), [&](auto al) {
     return go(combine_grad_kernel<R, O, TOK, DW, DR, decltype(al)::value>);
   });
 }
@@ -513,17 +515,17 @@ extern "C" int moe_dispatch(const void *x, int64_t x_stride, const float *x_scal
   // (M = 4096, hidden = 7168) 103.7 and 104.3.
   const int tok = M < 1024 || top_k > 6 ? 1 : 2;
   const dim3 grid((unsigned)pad_ctas(ceil_div64(M, tok), num_rows), s.parts), block(s.threads);
-  auto launch = [&](auto kernel) {
-    return launch_pdl(kernel, grid, block, 0, stream, a, static_cast<const char *>(x),
-                      x_stride * eb, x_scale, len, scales, static_cast<char *>(rows), rows_scale);
-  };
   auto go = [&](auto es, auto al) {
     constexpr int ES = decltype(es)::value, A = decltype(al)::value;
+    auto launch = [&](auto kernel) {
+      return launch_pdl(kernel, grid, block, 0, stream, a, static_cast<const char *>(x),
+                        x_stride * eb, x_scale, len / ES, scales, static_cast<char *>(rows),
+                        rows_scale);
+    };
     return tok == 2 ? launch(dispatch_kernel<ES, 2, A>) : launch(dispatch_kernel<ES, 1, A>);
   };
-  // by pieces and halves every type is the same
-  return by_align(align, [&](auto al) {
-    if constexpr (decltype(al)::value == kElems) {
+  return by_align(align, hidden, eb, [&](auto al) {
+    if constexpr (decltype(al)::value == kElems || decltype(al)::value == kDealt) {
       if (eb == 4) return go(std::integral_constant<int, 4>{}, al);
       if (eb == 2) return go(std::integral_constant<int, 2>{}, al);
     }

@@ -80,6 +80,8 @@ struct Split {
 // 448 threads at hidden = 7168 (M = 4096, E4M3) 38.9 us, four pieces for each of
 // 224 threads 47.1.  Gradient 512, up to 768 threads: at 896, with 72 registers
 // a thread instead of 80, hidden = 4096 (M = 10007) went from 55.6 to 71.4 us.
+// Widths that are dealt out by elements take 896 there too (hidden = 4097,
+// M = 8000: 193 us with four pieces a thread, 126 with two).
 Split split_row(int H, int per16, int two) {
   const int pieces = (H + per16 - 1) / per16;
   const int ch = pieces <= 256 ? 1 : pieces <= two ? 2 : pieces <= 2048 ? 4 : 8;
@@ -120,7 +122,7 @@ struct RowFeed {
   }
   __device__ __forceinline__ bool used() const { return in[IN - 1] != nullptr; }
   __device__ __forceinline__ bool on(int i) const {
-    return (int)(threadIdx.x + i * blockDim.x) < (H + N - 1) / N;
+    return in_row<N, A>(threadIdx.x + i * blockDim.x, H);
   }
   // Starts the copies of a row into the current stage (one group of copies,
   // empty if !live) and moves on to the next stage.
@@ -160,24 +162,24 @@ struct Weights {
   static constexpr bool kHeld = CH * N <= 16;
   f32x2 held[kHeld ? CH : 1][N / 2];
 
-  static __device__ __forceinline__ void read(const typename W::bits *w, int pieces, int H, int i,
+  static __device__ __forceinline__ void read(const typename W::bits *w, int H, int i,
                                               f32x2 (&f)[N / 2]) {
     const int c = threadIdx.x + i * blockDim.x;
-    raw_up<W, N>(c < pieces ? raw_load<W, N, A>(w, c, H) : raw_zero<W, N>(), f);
+    raw_up<W, N>(in_row<N, A>(c, H) ? raw_load<W, N, A>(w, c, H) : raw_zero<W, N>(), f);
   }
-  __device__ __forceinline__ void load(const typename W::bits *w, int pieces, int H) {
+  __device__ __forceinline__ void load(const typename W::bits *w, int H) {
     if constexpr (kHeld) {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) read(w, pieces, H, i, held[i]);
+      for (int i = 0; i < CH; ++i) read(w, H, i, held[i]);
     }
   }
-  __device__ __forceinline__ void get(const typename W::bits *w, int pieces, int H, int i,
+  __device__ __forceinline__ void get(const typename W::bits *w, int H, int i,
                                       f32x2 (&f)[N / 2]) const {
     if constexpr (kHeld) {
 #pragma unroll
       for (int e = 0; e < N / 2; ++e) f[e] = held[i][e];
     } else {
-      read(w, pieces, H, i, f);
+      read(w, H, i, f);
     }
   }
 };
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(CH <= 2 ? 448 : 512, CH <= 2 ? 2 : 1)
   __shared__ __align__(16) float red[2][kRedFloats];
   pdl_wait();
   pdl_trigger();
-  const int H = a.H, pieces = (H + N - 1) / N, tid = threadIdx.x, tpr = blockDim.x;
+  const int H = a.H, tid = threadIdx.x, tpr = blockDim.x;
   const WB *w = static_cast<const WB *>(a.w);
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(CH <= 2 ? 448 : 512, CH <= 2 ? 2 : 1)
   feed.init(ring);
   for (int d = 0; d < a.depth; ++d) feed.start(row + d * step, row + d * step < a.M);
   Weights<W, N, CH, A> weights;
-  weights.load(w, pieces, H);
+  weights.load(w, H);
   clear_red(red);
   int turn = 0;
   for (; row < a.M; row += step) {
@@ -256,9 +258,9 @@ __global__ void __launch_bounds__(CH <= 2 ? 448 : 512, CH <= 2 ? 2 : 1)
         sr[i] = feed.get(row, 0, i);
         // the sum as it is stored is what is normalised
         if (feed.used()) sr[i] = raw_add<T, N>(sr[i], feed.get(row, 1, i));
+        if (a.sum)
+          raw_store<T, N, A>(static_cast<TB *>(a.sum) + out_at, tid + i * tpr, H, sr[i]);
       }
-      if (a.sum)
-        raw_store<T, N, A>(static_cast<TB *>(a.sum) + out_at, tid + i * tpr, H, sr[i], feed.on(i));
       f32x2 f[N / 2];
       raw_up<T, N>(sr[i], f);
 #pragma unroll
@@ -278,38 +280,47 @@ __global__ void __launch_bounds__(CH <= 2 ? 448 : 512, CH <= 2 ? 2 : 1)
       const bool on = feed.on(i);
       f32x2 f[N / 2], wf[N / 2];
       raw_up<T, N>(sr[i], f);
-      weights.get(w, pieces, H, i, wf);
-      if (a.out) {
+      weights.get(w, H, i, wf);
+      if (a.out && on) {
         f32x2 v[N / 2];
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) v[e] = mul2(mul2(f[e], pair(rstd, rstd)), wf[e]);
-        raw_store<T, N, A>(static_cast<TB *>(a.out) + out_at, c, H, raw_down<T>(v), on);
+        raw_store<T, N, A>(static_cast<TB *>(a.out) + out_at, c, H, raw_down<T>(v));
       }
       if (a.codes) {
-        float m = 0.f;
+        // Blocks of 128 columns: 128 / N lanes hold one; dealt out, a lane has
+        // four elements of each of N / 4 blocks.
+        constexpr int B = A == kDealt ? N / 4 : 1, G = N / B;   // blocks of a piece, elements each
 #pragma unroll
-        for (int e = 0; e < N / 2; ++e) {
-          f[e] = mul2(f[e], wf[e]);
-          const float2 p = unpair(f[e]);
-          m = max_abs_nan(m, p.x, p.y);
-        }
-        // the 128 / N threads of a block of 128 columns
+        for (int b = 0; b < B; ++b) {
+          float m = 0.f;
 #pragma unroll
-        for (int d = 64 / N; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, d));
-        float sc = m * rstd / kE4m3Max;
-        if (sc >= kScaleMin && m >= 0x1p-100f && m <= 0x1p100f) {
-          const float y = 1.f / m;
-#pragma unroll
-          for (int e = 0; e < N / 2; ++e) f[e] = code_quotient(f[e], pair(-m, -m), pair(y, y));
-        } else {   // scales at their floor, and extremes of s * w
-          const bool low = sc < kScaleMin;
-#pragma unroll
-          for (int e = 0; e < N / 2; ++e) {
+          for (int e = b * G / 2; e < (b + 1) * G / 2; ++e) {
+            f[e] = mul2(f[e], wf[e]);
             const float2 p = unpair(f[e]);
-            f[e] = low ? pair(p.x * rstd / kScaleMin, p.y * rstd / kScaleMin)
-                       : pair(p.x * kE4m3Max / m, p.y * kE4m3Max / m);
+            m = max_abs_nan(m, p.x, p.y);
           }
-          if (low) sc = kScaleMin;
+#pragma unroll
+          for (int d = 64 / G; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, d));
+          float sc = m * rstd / kE4m3Max;
+          if (sc >= kScaleMin && m >= 0x1p-100f && m <= 0x1p100f) {
+            const float y = 1.f / m;
+#pragma unroll
+            for (int e = b * G / 2; e < (b + 1) * G / 2; ++e)
+              f[e] = code_quotient(f[e], pair(-m, -m), pair(y, y));
+          } else {   // scales at their floor, and extremes of s * w
+            const bool low = sc < kScaleMin;
+#pragma unroll
+            for (int e = b * G / 2; e < (b + 1) * G / 2; ++e) {
+              const float2 p = unpair(f[e]);
+              f[e] = low ? pair(p.x * rstd / kScaleMin, p.y * rstd / kScaleMin)
+                         : pair(p.x * kE4m3Max / m, p.y * kE4m3Max / m);
+            }
+            if (low) sc = kScaleMin;
+          }
+          // the lane that holds a block's first element
+          if (const int x = place<N, A>(c, b * G); x < H && x % 128 == 0)
+            a.scale[row * ((H + 127) / 128) + x / 128] = sc;
         }
         uint32_t q[N / 4];
 #pragma unroll
@@ -318,18 +329,17 @@ __global__ void __launch_bounds__(CH <= 2 ? 448 : 512, CH <= 2 ? 2 : 1)
           q[e] = to_e4m3x2(lo.x, lo.y) | ((uint32_t)to_e4m3x2(hi.x, hi.y) << 16);
         }
         if (on) {
-          uint8_t *dst = a.codes + out_at + (size_t)c * N;
+          uint8_t *dst = a.codes + out_at;
           if constexpr (A != kWhole) {
-            const int left = H - c * N;
 #pragma unroll
             for (int e = 0; e < N; ++e)
-              if (e < left) dst[e] = (uint8_t)(q[e / 4] >> (8 * (e & 3)));
+              if (const int x = place<N, A>(c, e); x < H)
+                dst[x] = (uint8_t)(q[e / 4] >> (8 * (e & 3)));
           } else if constexpr (N == 8) {
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(q[0], q[1]);
+            *reinterpret_cast<uint2 *>(dst + (size_t)c * N) = make_uint2(q[0], q[1]);
           } else {
-            *reinterpret_cast<uint32_t *>(dst) = q[0];
+            *reinterpret_cast<uint32_t *>(dst + (size_t)c * N) = q[0];
           }
-          if (tid % (128 / N) == 0) a.scale[row * ((H + 127) / 128) + c / (128 / N)] = sc;
         }
       }
     }
@@ -370,7 +380,7 @@ __global__ void __launch_bounds__(grad_threads(CH)) rmsnorm_grad_kernel(NormGrad
   __shared__ __align__(16) float red[2][kRedFloats];
   pdl_wait();
   pdl_trigger();
-  const int H = a.H, pieces = (H + N - 1) / N, tid = threadIdx.x, tpr = blockDim.x;
+  const int H = a.H, tid = threadIdx.x, tpr = blockDim.x;
   const WB *w = static_cast<const WB *>(a.w);
   f32x2 dw[CH][N / 2] = {};
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
@@ -383,7 +393,7 @@ __global__ void __launch_bounds__(grad_threads(CH)) rmsnorm_grad_kernel(NormGrad
   feed.init(ring);
   for (int d = 0; d < a.depth; ++d) feed.start(row + d * step, row + d * step < a.M);
   Weights<W, N, CH, A> weights;
-  weights.load(w, pieces, H);
+  weights.load(w, H);
   clear_red(red);
   int turn = 0;
   float next = row < a.M ? a.rstd[row] : 0.f;   // rstd, read a row ahead
@@ -397,16 +407,13 @@ __global__ void __launch_bounds__(grad_threads(CH)) rmsnorm_grad_kernel(NormGrad
     f32x2 dot = 0;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      if (!feed.on(i)) {
-        if constexpr (A != kWhole) dr[i] = sr[i] = raw_zero<T, N>();
-        continue;
-      }
+      if (!feed.on(i)) continue;
       dr[i] = feed.get(row, 0, i);
       sr[i] = feed.get(row, 1, i);
       f32x2 d[N / 2], xh[N / 2], wf[N / 2];
       raw_up<T, N>(dr[i], d);
       raw_up<T, N>(sr[i], xh);
-      weights.get(w, pieces, H, i, wf);
+      weights.get(w, H, i, wf);
 #pragma unroll
       for (int e = 0; e < N / 2; ++e) {
         xh[e] = mul2(xh[e], rstd2);
@@ -420,17 +427,16 @@ __global__ void __launch_bounds__(grad_threads(CH)) rmsnorm_grad_kernel(NormGrad
     const float back = -(rstd * rstd * mean);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      if (A == kWhole && !feed.on(i)) continue;   // else whole warps up to the store
+      if (!feed.on(i)) continue;
       f32x2 d[N / 2], s[N / 2], wf[N / 2], v[N / 2] = {};
       raw_up<T, N>(dr[i], d);
       raw_up<T, N>(sr[i], s);
-      if (feed.used() && feed.on(i)) raw_up<T, N>(feed.get(row, 2, i), v);
-      weights.get(w, pieces, H, i, wf);
+      if (feed.used()) raw_up<T, N>(feed.get(row, 2, i), v);
+      weights.get(w, H, i, wf);
 #pragma unroll
       for (int e = 0; e < N / 2; ++e)
         v[e] = fma2(s[e], pair(back, back), fma2(rstd2, mul2(d[e], wf[e]), v[e]));
-      raw_store<T, N, A>(static_cast<TB *>(a.dx) + out_at, tid + i * tpr, H, raw_down<T>(v),
-                         feed.on(i));
+      raw_store<T, N, A>(static_cast<TB *>(a.dx) + out_at, tid + i * tpr, H, raw_down<T>(v));
     }
     // the slots of this row have been read: the row `depth` turns on goes there
     feed.start(row + a.depth * step, row + a.depth * step < a.M);
@@ -457,8 +463,10 @@ __global__ void __launch_bounds__(grad_threads(CH)) rmsnorm_grad_kernel(NormGrad
 #pragma unroll
       for (int e = 0; e < N / 2; ++e) {
         const float2 v = unpair(dw[i][e]);
-        if (h + 2 * e < H) mine[h + 2 * e] = v.x;
-        if (h + 2 * e + 1 < H) mine[h + 2 * e + 1] = v.y;
+        const int c = tid + i * tpr;
+        const int x = place<N, A>(c, 2 * e), y = place<N, A>(c, 2 * e + 1);
+        if (x < H) mine[x] = v.x;
+        if (y < H) mine[y] = v.y;
       }
     }
   }
@@ -596,15 +604,16 @@ extern "C" int moe_add_rmsnorm(const void *x, int64_t x_stride, const void *resi
       const int rc = ensure_smem_limit((const void *)kernel, smem + kStaticBytes);
       return rc ? rc : launch_pdl(kernel, grid, block, smem, stream, a);
     };
-    if (s.ch == 1) return by_align(
-          align, [&](auto al) { return go(add_rmsnorm_kernel<T, W, 1, decltype(al)::value>); });
-    if (s.ch == 2) return by_align(
-          align, [&](auto al) { return go(add_rmsnorm_kernel<T, W, 2, decltype(al)::value>); });
-    if (s.ch == 4) return by_align(
-          align, [&](auto al) { return go(add_rmsnorm_kernel<T, W, 4, decltype(al)::value>); });
+    auto with = [&](auto ch) {
+      return by_align(align, hidden, b, [&](auto al) {
+        return go(add_rmsnorm_kernel<T, W, decltype(ch)::value, decltype(al)::value>);
+      });
+    };
+    if (s.ch == 1) return with(std::integral_constant<int, 1>{});
+    if (s.ch == 2) return with(std::integral_constant<int, 2>{});
+    if (s.ch == 4) return with(std::integral_constant<int, 4>{});
     if constexpr (sizeof(typename T::bits) == 4)   // fp32 rows above 8192
-      return by_align(
-          align, [&](auto al) { return go(add_rmsnorm_kernel<T, W, 8, decltype(al)::value>); });
+      return with(std::integral_constant<int, 8>{});
     return MOE_EUNSUPPORTED;
   });
 }
@@ -639,7 +648,7 @@ extern "C" int moe_add_rmsnorm_backward(const void *dout, int64_t dout_stride, c
       (dsum && dsum_stride != hidden && dsum == dx))
     return MOE_EINVAL;
   const int n = 16 / b;
-  const Split s = split_row(hidden, n, kTwoGradient);
+  const Split s = split_row(hidden, n, hidden * b % 8 ? kTwoForward : kTwoGradient);
   int align = rows_alignment(dout, dout_stride, hidden, b);
   for (const int k : {rows_alignment(sum, sum_stride, hidden, b),
                       rows_alignment(dsum, dsum_stride, hidden, b),
@@ -665,15 +674,16 @@ extern "C" int moe_add_rmsnorm_backward(const void *dout, int64_t dout_stride, c
         const int r = ensure_smem_limit((const void *)kernel, smem + kStaticBytes);
         return r ? r : launch_pdl(kernel, grid, block, smem, stream, a);
       };
-      if (s.ch == 1) return by_align(
-          align, [&](auto al) { return go(rmsnorm_grad_kernel<T, W, 1, decltype(al)::value>); });
-      if (s.ch == 2) return by_align(
-          align, [&](auto al) { return go(rmsnorm_grad_kernel<T, W, 2, decltype(al)::value>); });
-      if (s.ch == 4) return by_align(
-          align, [&](auto al) { return go(rmsnorm_grad_kernel<T, W, 4, decltype(al)::value>); });
+      auto with = [&](auto ch) {
+        return by_align(align, hidden, b, [&](auto al) {
+          return go(rmsnorm_grad_kernel<T, W, decltype(ch)::value, decltype(al)::value>);
+        });
+      };
+      if (s.ch == 1) return with(std::integral_constant<int, 1>{});
+      if (s.ch == 2) return with(std::integral_constant<int, 2>{});
+      if (s.ch == 4) return with(std::integral_constant<int, 4>{});
       if constexpr (sizeof(typename T::bits) == 4)   // fp32 rows above 8192
-        return by_align(
-          align, [&](auto al) { return go(rmsnorm_grad_kernel<T, W, 8, decltype(al)::value>); });
+        return with(std::integral_constant<int, 8>{});
       return MOE_EUNSUPPORTED;
     });
     if (rc) return rc;

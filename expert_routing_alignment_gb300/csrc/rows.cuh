@@ -117,25 +117,29 @@ __device__ __forceinline__ Raw<T, N> raw_load_aligned(const void *p) {
 
 // ---- pieces by alignment ------------------------------------------------------
 //
-// How the pieces of a call's rows can be moved: whole (16-byte aligned rows of
-// whole pieces), as 8-byte halves (8-byte aligned, a multiple of 8 bytes), or
-// element by element.
-enum { kWhole = 16, kHalves = 8, kElems = 1 };
+// How the pieces of a call's rows are held and moved:
+//   kWhole   16-byte aligned rows of whole pieces;
+//   kHalves  8-byte aligned rows of whole 8-byte halves, two of them a piece;
+//   kElems   such widths at any other alignment, element by element;
+//   kDealt   other widths, element by element and dealt out in turn: element i
+//            of a lane's piece is the (32 i + lane)th of the 32 N that a warp
+//            holds, so that a warp's loads and stores are runs of neighbours (a
+//            lane with N neighbours of its own makes four times the memory
+//            wavefronts: the bf16 combine gradient at M = 2000, hidden = 1111,
+//            top_k = 6 took 42.6 us, dealt out it takes 29.3).
+// Which elements a thread holds depends on the width alone, not on the
+// alignment, so neither do a sum's bits.
+enum { kWhole = 16, kHalves = 8, kDealt = 2, kElems = 1 };
 
-// Bytes [n, n + 16) of the 32 bytes lo, hi; 0 <= n < 16.
-__device__ __forceinline__ uint4 bytes_from(const uint4 &lo, const uint4 &hi, int n) {
-  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  if (n & 8) {
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  }
-  if (n & 4) {
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  }
-  const int s = (n & 3) * 8;
-  return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s),
-                    __funnelshift_r(w[2], w[3], s), __funnelshift_r(w[3], w[4], s));
+// Element i of piece c: its place in the row.
+template <int N, int A>
+__device__ __forceinline__ int place(int c, int i) {
+  return A == kDealt ? (c & ~31) * N + (c & 31) + 32 * i : c * N + i;
+}
+// Whether piece c has an element of the row.
+template <int N, int A>
+__device__ __forceinline__ bool in_row(int c, int H) {
+  return place<N, A>(c, 0) < H;
 }
 
 template <int ES> struct Elem;
@@ -151,98 +155,54 @@ __device__ __forceinline__ typename Elem<ES>::type elem_of(const uint4 &q, int i
   return (typename Elem<ES>::type)(w >> (8 * (b & 3)));
 }
 
-// The 16 bytes at byte `at` (a multiple of 16) of a row of `len` bytes, zeros
-// behind its end.
+// Piece c of a row of H elements of ES bytes, zeros behind its end.
 template <int ES, int A>
-__device__ __forceinline__ uint4 load16(const void *row, int at, int len) {
-  const char *p = static_cast<const char *>(row) + at;
+__device__ __forceinline__ uint4 load16(const void *row, int c, int H) {
+  constexpr int N = 16 / ES;
+  const char *p = static_cast<const char *>(row) + (size_t)c * 16;
   if constexpr (A == kWhole) {
     return *reinterpret_cast<const uint4 *>(p);
   } else if constexpr (A == kHalves) {
     const uint2 lo = *reinterpret_cast<const uint2 *>(p);
-    const uint2 hi = at + 8 < len ? reinterpret_cast<const uint2 *>(p)[1] : make_uint2(0, 0);
+    const uint2 hi = c * N + N / 2 < H ? reinterpret_cast<const uint2 *>(p)[1] : make_uint2(0, 0);
     return make_uint4(lo.x, lo.y, hi.x, hi.y);
   } else {
+    const int first = place<N, A>(c, 0), left = H - first;
+    const typename Elem<ES>::type *e = static_cast<const typename Elem<ES>::type *>(row) + first;
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 16 / ES; ++i)
-      if (at + i * ES < len)
-        w[i * ES / 4] |= (uint32_t)reinterpret_cast<const typename Elem<ES>::type *>(p)[i]
-                         << (8 * (i * ES & 3));
+    for (int i = 0; i < N; ++i)
+      if (place<N, A>(0, i) < left)
+        w[i * ES / 4] |= (uint32_t)e[place<N, A>(0, i)] << (8 * (i * ES & 3));
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
-
-// Writes 16 bytes q at byte `at` of a row that is moved element by element:
-// what lies inside the row, nothing outside.  A whole warp, whose lanes hold
-// consecutive pieces; lanes that are not `on`, the last ones, hold none.  A
-// piece lies across two aligned 16-byte windows: the lanes hand their ends on
-// and write by window, single elements only at the ends of the row and of the
-// warp (the combine gradient's fp16 rows of 2884: 117 us by elements, 81 by
-// windows).  Not inlined: the callers' unrolled loops hold eight of them.
-template <int ES>
-__device__ __noinline__ void store16_elems(void *row, int at, int len, uint4 q, bool on) {
-  using E = typename Elem<ES>::type;
-  char *p = static_cast<char *>(row) + at;
-  const int off = (int)((uintptr_t)row & 15);   // the warp's: `at` is a multiple of 16
-  const int mine = len - at < 16 ? len - at : 16;   // bytes of the piece
-  const int lane = threadIdx.x & 31, head = 16 - off;   // the piece's bytes in its first window
-  int from = 16, to = mine;   // what is written by elements
-  if (off == 0) {
-    if (!on) return;
-    if (mine == 16)
-      *reinterpret_cast<uint4 *>(p) = q;
-    else
-      from = 0;
-  } else {
-    uint4 prev;
-    prev.x = __shfl_up_sync(0xFFFFFFFFu, q.x, 1);
-    prev.y = __shfl_up_sync(0xFFFFFFFFu, q.y, 1);
-    prev.z = __shfl_up_sync(0xFFFFFFFFu, q.z, 1);
-    prev.w = __shfl_up_sync(0xFFFFFFFFu, q.w, 1);
-    if (!on) return;
-    const bool last = lane == 31 || at + 16 >= len;   // no lane takes this one's tail
-    if (lane == 0) {
-      from = 0;   // its window is shared with the warp before
-      if (!last && to > head) to = head;
-    } else if (mine >= head) {
-      *reinterpret_cast<uint4 *>(p - off) = bytes_from(prev, q, head);
-      if (last) from = head;
-    } else {   // the row ends in the window: the neighbour's tail, too
-      from = 0;
-#pragma unroll
-      for (int i = 0; i < 16 / ES; ++i)
-        if (i * ES >= head) reinterpret_cast<E *>(p - 16)[i] = elem_of<ES>(prev, i);
-    }
-  }
-  if (from < to) {
-#pragma unroll
-    for (int i = 0; i < 16 / ES; ++i)
-      if (i * ES >= from && i * ES < to) reinterpret_cast<E *>(p)[i] = elem_of<ES>(q, i);
-  }
-}
-
 template <int ES, int A>
-__device__ __forceinline__ void store16(void *row, int at, int len, const uint4 &q, bool on) {
-  char *p = static_cast<char *>(row) + at;
+__device__ __forceinline__ void store16(void *row, int c, int H, const uint4 &q) {
+  constexpr int N = 16 / ES;
+  char *p = static_cast<char *>(row) + (size_t)c * 16;
   if constexpr (A == kWhole) {
-    if (on) *reinterpret_cast<uint4 *>(p) = q;
+    *reinterpret_cast<uint4 *>(p) = q;
   } else if constexpr (A == kHalves) {
-    if (on) *reinterpret_cast<uint2 *>(p) = make_uint2(q.x, q.y);
-    if (on && at + 8 < len) reinterpret_cast<uint2 *>(p)[1] = make_uint2(q.z, q.w);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(q.x, q.y);
+    if (c * N + N / 2 < H) reinterpret_cast<uint2 *>(p)[1] = make_uint2(q.z, q.w);
   } else {
-    store16_elems<ES>(row, at, len, q, on);
+    const int first = place<N, A>(c, 0), left = H - first;
+    typename Elem<ES>::type *e = static_cast<typename Elem<ES>::type *>(row) + first;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (place<N, A>(0, i) < left) e[place<N, A>(0, i)] = elem_of<ES>(q, i);
   }
 }
 
 // Piece c (N elements, 16 bytes, or 8 in the 16-bit type of a mixed pair) of a
-// row of H elements; zeros behind the end.  Plain (coherent) loads: some
+// row of H elements, in_row; zeros behind the end.  Plain (coherent) loads: some
 // callers let an output share an input's buffer.
 template <typename T, int N, int A>
 __device__ __forceinline__ Raw<T, N> raw_load(const typename T::bits *row, int c, int H) {
   constexpr int ES = sizeof(typename T::bits);
   if constexpr (N * ES == 16) {
-    const uint4 q = load16<ES, A>(row, c * 16, H * ES);
+    const uint4 q = load16<ES, A>(row, c, H);
     return Raw<T, N>{{q.x, q.y, q.z, q.w}};
   } else if constexpr (A == kWhole) {
     return raw_load_aligned<T, N>(row + (size_t)c * N);
@@ -250,25 +210,23 @@ __device__ __forceinline__ Raw<T, N> raw_load(const typename T::bits *row, int c
     Raw<T, N> r = raw_zero<T, N>();
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (c * N + i < H) r.w[i * ES / 4] |= (uint32_t)row[(size_t)c * N + i] << (8 * (i * ES & 3));
+      if (const int e = place<N, A>(c, i); e < H)
+        r.w[i * ES / 4] |= (uint32_t)row[e] << (8 * (i * ES & 3));
     return r;
   }
 }
-
-// kElems: a whole warp, as store16_elems.
 template <typename T, int N, int A>
-__device__ __forceinline__ void raw_store(typename T::bits *row, int c, int H, const Raw<T, N> &r,
-                                          bool on) {
+__device__ __forceinline__ void raw_store(typename T::bits *row, int c, int H, const Raw<T, N> &r) {
   constexpr int ES = sizeof(typename T::bits);
-  typename T::bits *p = row + (size_t)c * N;
   if constexpr (N * ES == 16) {
-    store16<ES, A>(row, c * 16, H * ES, make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]), on);
+    store16<ES, A>(row, c, H, make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]));
   } else if constexpr (A == kWhole) {
-    if (on) *reinterpret_cast<uint2 *>(p) = make_uint2(r.w[0], r.w[1]);
-  } else if (on) {
+    *reinterpret_cast<uint2 *>(row + (size_t)c * N) = make_uint2(r.w[0], r.w[1]);
+  } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (c * N + i < H) p[i] = (typename T::bits)(r.w[i * ES / 4] >> (8 * (i * ES & 3)));
+      if (const int e = place<N, A>(c, i); e < H)
+        row[e] = (typename T::bits)(r.w[i * ES / 4] >> (8 * (i * ES & 3)));
   }
 }
 
@@ -346,7 +304,7 @@ __device__ __forceinline__ Raw<T, N> raw_down(const float (&f)[N]) {
 // copies themselves.
 
 constexpr int kMaxDepth = 4;            // groups in flight
-constexpr size_t kStaticBytes = 20480;  // more than a kernel's other shared memory, with which
+constexpr size_t kStaticBytes = 2048;   // more than a kernel's other shared memory, with which
                                         // the ring shares its limit
 
 __device__ __forceinline__ void copy16_async(uint32_t shared, const void *global) {
@@ -393,13 +351,15 @@ inline int rows_alignment(const void *p, int64_t stride, int hidden, int bytes) 
                      (uint64_t)hidden * bytes | 16;
   return (int)(v & (~v + 1));
 }
-// f(integral_constant of kWhole, kHalves or kElems) for an alignment in bytes;
-// MIXED: pairs of types, which have no halves.
+// f(integral_constant of how the pieces are moved) for an alignment in bytes of
+// rows of `hidden` elements of `bytes`; MIXED: pairs of types, whose pieces have
+// no halves.
 template <bool MIXED = false, typename F>
-int by_align(int align, F &&f) {
+int by_align(int align, int hidden, int bytes, F &&f) {
   if (align == 16) return f(std::integral_constant<int, kWhole>{});
   if constexpr (!MIXED)
     if (align == 8) return f(std::integral_constant<int, kHalves>{});
+  if (hidden * bytes % (MIXED ? 16 : 8)) return f(std::integral_constant<int, kDealt>{});
   return f(std::integral_constant<int, kElems>{});
 }
 
