@@ -479,14 +479,16 @@ _FLOAT = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: D
 _ROWS = {**_FLOAT, torch.float8_e4m3fn: DTYPE_E4M3, torch.uint8: DTYPE_E4M3}
 
 # These wrappers stand in front of kernels of a few microseconds, so they pass
-# plain addresses, check each tensor once and ask for the current stream's
-# handle directly (a torch.cuda.Stream object costs more than the launch).
+# plain addresses, check each tensor once and ask for the current device and
+# stream directly (a torch.cuda.Stream object costs more than the launch).
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _on_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
     """The kernels run on the current device: refuse tensors of any other."""
     dev = first.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != _current_device():
         raise ValueError(f"want CUDA tensors of the current device, got one on {first.device}")
     for t in others:
         if t is not None and t.get_device() != dev:
@@ -497,7 +499,7 @@ def _on_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
 def _handle(stream, dev: int) -> int:
     """The cudaStream_t of a stream argument; None: the device's current one."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _current_stream(dev)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -746,8 +748,8 @@ def moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     if residual is not None:
         rs, r_at = _row_stride("residual", residual, dtype, (M, H)), residual.data_ptr()
     w_at = _at("weight", weight, weight.dtype, (H,))
+    at = {}
     if out is not None:
-        at = {}
         for name, t in out.items():
             shape, otype = _norm_output(name, dtype, M, H)
             if name == "codes" and t.dtype is torch.uint8:
@@ -755,10 +757,11 @@ def moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
             at[name] = _at(name, t, otype, shape)
         dev = _on_device(x, weight, residual, *out.values())
     else:
-        dev = _on_device(x, weight, residual)
-        device = x.device
-        out = {name: _empty(*_norm_output(name, dtype, M, H), device, stream) for name in want}
-        at = {name: t.data_ptr() for name, t in out.items()}
+        dev, device, out = _on_device(x, weight, residual), x.device, {}
+        for name in want:
+            shape, otype = _norm_output(name, dtype, M, H)
+            t = out[name] = _empty(shape, otype, device, stream)
+            at[name] = t.data_ptr()
     get = at.get
     _check("moe_add_rmsnorm", load().moe_add_rmsnorm(
         x.data_ptr(), xs, r_at, rs, w_at, kind, wkind, M, H, eps, get("sum"), get("out"),

@@ -446,9 +446,9 @@ int moe_decode_layer_noalloc(const moe_layer_desc *layer, const uint16_t *x, int
  *    grouped product over whole blocks reads no garbage; rows at or past the
  *    total stay as they were.  Padding rows of inputs are never read.
  *  - M = 0 is valid.  1 <= top_k <= 32, M * top_k <= MOE_MAX_SLOTS, any hidden
- *    from 1 to MOE_MAX_ROW_HIDDEN: rows that are whole 16-byte pieces (16-byte
- *    aligned, hidden a multiple of 8) take the fast path, others are served
- *    element by element.
+ *    from 1 to MOE_MAX_ROW_HIDDEN and any alignment of rows to their elements:
+ *    rows of whole 16-byte pieces, 16-byte aligned, are the fast ones, then
+ *    those of whole 8-byte halves.
  *  - A *_stride is the distance of the rows of an input in elements, >= 0 (0:
  *    one row for all).  Outputs and expert-order buffers are dense, and
  *    overlap no input unless stated.
@@ -544,8 +544,8 @@ int moe_topk_softmax_backward(const int32_t *topk_ids, const float *topk_w,
  *   output may be NULL, not all of them.  sum_out and out are different
  *   buffers; either may be x's or residual's own when that input is dense
  *   (stride = hidden).
- * M = 0 is valid; any hidden from 1 to MOE_MAX_ROW_HIDDEN, whole 16-byte
- * pieces fast as above; a row's bits do not depend on M.
+ * M = 0 is valid; any hidden from 1 to MOE_MAX_ROW_HIDDEN, fast as above; a
+ * row's bits do not depend on M.
  * Errors: MOE_EINVAL (NULL, sizes, strides, eps negative or not finite, one of
  * codes and scale alone, sum_out and out the same, a strided input shared with
  * an output, misaligned),

@@ -673,6 +673,28 @@ def test_add_rmsnorm_gradient_of_many_rows_is_the_same_every_time():
     assert torch.equal(bits(a), bits(dx)) and torch.equal(bits(b), bits(dw))
 
 
+@pytest.mark.parametrize("H", [256, 2884, 77])
+def test_add_rmsnorm_gradient_of_broadcast_rows(H):
+    """A gradient that is one row for all (stride 0), as a sum's is, and a
+    strided sum; the same bits as from dense copies."""
+    M = 37
+    x, s, w = norm_inputs(M, H, BF, FL, 450)
+    rstd = (1 / torch.sqrt(s.double().square().mean(1) + 1e-6)).float()
+    wide = torch.zeros(M, H + 24, dtype=BF, device="cuda")
+    wide[:, 8: 8 + H] = s
+    one = x[:1].expand(M, H)
+    a, b = moe.moe_add_rmsnorm_backward(one, wide[:, 8: 8 + H], w, rstd, dsum=one)
+    c, d = moe.moe_add_rmsnorm_backward(one.contiguous(), s, w, rstd, dsum=one.contiguous())
+    assert torch.equal(bits(a), bits(c)) and torch.equal(bits(b), bits(d))
+    # a workspace for more rows serves fewer
+    ws = torch.empty(moe.add_rmsnorm_backward_workspace_bytes(10 * M, H), dtype=torch.uint8,
+                     device="cuda")
+    for n in (1, 5, M):
+        p = moe.moe_add_rmsnorm_backward(x[:n], s[:n], w, rstd[:n], workspace=ws)
+        q = moe.moe_add_rmsnorm_backward(x[:n], s[:n], w, rstd[:n])
+        assert torch.equal(bits(p[0]), bits(q[0])) and torch.equal(bits(p[1]), bits(q[1]))
+
+
 def test_add_rmsnorm_gradient_against_differences():
     """fp32 rows against central differences of the float64 norm, along random
     directions of the input and of the weight."""
