@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(256) combine_kernel(SlotArgs a, const typename
 // sums), the warps' sums are added in warp order.  A sum's order depends on
 // hidden and the type alone: a token's bits are the same in every batch.
 // Bound by HBM: bf16 at M = 16384, hidden = 4096, top_k = 8 (2.42 GB, half of
-// it written) 365 us, 6.6 TB/s; three CTAs an SM (72 registers), since 96
+// it written) 365 us, 6.6 TB/s; three CTAs an SM (80 registers), since 96
 // registers and two CTAs took 408 us.  Weights alone (fp32 rows, M = 512,
 // hidden = 4096: 71 MB) 14 us, 5.1 TB/s, one wave of four CTAs an SM.
 
