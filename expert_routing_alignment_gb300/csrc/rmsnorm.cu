@@ -98,14 +98,19 @@ int plan_depth(size_t stage, int groups, int64_t turns, int flight) {
 }
 
 // The rows of IN input arrays (the last may be NULL: not used), as the walk
-// above feeds them (kWhole), or read straight from global memory.  In a stage
+// above feeds them, or, by elements of two bytes, which no copy moves, read
+// straight from global memory.  (Straight against ahead: bf16 in halves, M = 8000,
+// hidden = 4100, 56.6 us and 48.6, gradient 112 and 67; fp32 by elements,
+// hidden = 4097, 200 and 122, gradient 296 and 130; calls of one row a group are
+// up to 0.8 us slower ahead, fp32 M = 400, hidden = 1001: 2.6 and 3.4.)  In a stage
 // the slots of neighbouring threads are next to one another: copies and reads
 // of a warp are whole lines.  (Slots by thread, 112 bytes apart, took the
 // gradient at M = 10007, hidden = 4096 from 56 to 85 us.)
 template <typename T, int IN, int CH, int A>
 struct RowFeed {
-  static constexpr int N = kPer16<T>;
   using TB = typename T::bits;
+  static constexpr int N = kPer16<T>;
+  static constexpr bool kAhead = kCopied<sizeof(TB), A>;
   const TB *in[IN];
   int64_t stride[IN];
   int H, depth;
@@ -127,15 +132,17 @@ struct RowFeed {
   // Starts the copies of a row into the current stage (one group of copies,
   // empty if !live) and moves on to the next stage.
   __device__ __forceinline__ void start(int64_t row, bool live) {
-    if constexpr (A == kWhole) {
+    if constexpr (kAhead) {
       if (live) {
 #pragma unroll
         for (int a = 0; a < IN; ++a) {
           if (a == IN - 1 && !used()) continue;
-          const TB *p = in[a] + row * stride[a] + threadIdx.x * N;
+          const TB *p = in[a] + row * stride[a];
 #pragma unroll
           for (int i = 0; i < CH; ++i)
-            if (on(i)) copy16_async(at + (a * CH + i) * unit(), p + i * blockDim.x * N);
+            if (on(i))
+              copy_piece_async<sizeof(TB), A>(at + (a * CH + i) * unit(), p,
+                                              threadIdx.x + i * blockDim.x, H);
         }
       }
       copies_commit();
@@ -144,11 +151,11 @@ struct RowFeed {
     }
   }
   __device__ __forceinline__ void wait() const {
-    if constexpr (A == kWhole) copies_wait(depth);
+    if constexpr (kAhead) copies_wait(depth);
   }
   // This thread's piece i (on(i)) of array a, row `row` in the current stage.
   __device__ __forceinline__ Raw<T, N> get(int64_t row, int a, int i) const {
-    if constexpr (A == kWhole)
+    if constexpr (kAhead)
       return raw_load_shared<T>(at + (a * CH + i) * unit());
     else
       return raw_load<T, N, A>(in[a] + row * stride[a], threadIdx.x + i * blockDim.x, H);
@@ -596,7 +603,7 @@ extern "C" int moe_add_rmsnorm(const void *x, int64_t x_stride, const void *resi
   const NormArgs a{x,   residual, weight,    x_stride,  residual_stride, M, hidden, depth,
                    eps, 1.f / hidden, sum_out, out, out_codes, out_scale, rstd};
   const dim3 grid((unsigned)ctas), block(s.tpr, rows);
-  const size_t smem = align == kWhole ? depth * stage : 0;
+  const size_t smem = can_copy(align, b) ? depth * stage : 0;
   return with_norm_types(dtype, weight_dtype, [&](auto t, auto w) {
     using T = decltype(t);
     using W = decltype(w);
@@ -661,7 +668,7 @@ extern "C" int moe_add_rmsnorm_backward(const void *dout, int64_t dout_stride, c
     const size_t stage = (size_t)3 * s.ch * s.tpr * walk.groups * 16;
     const int64_t turns = ceil_div64(M, (int64_t)walk.ctas * walk.groups);
     const int depth = plan_depth(stage, 1, turns, 144 * 1024);
-    const size_t ring = align == kWhole ? depth * stage : 0;
+    const size_t ring = can_copy(align, b) ? depth * stage : 0;
     const size_t parts = walk.groups > 1 ? (size_t)walk.groups * hidden * sizeof(float) : 0;
     const size_t smem = ring > parts ? ring : parts;
     const NormGradArgs a{dout, sum,    dsum,  weight, rstd, dout_stride, sum_stride, dsum_stride,

@@ -310,6 +310,38 @@ constexpr size_t kStaticBytes = 2048;   // more than a kernel's other shared mem
 __device__ __forceinline__ void copy16_async(uint32_t shared, const void *global) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(shared), "l"(global) : "memory");
 }
+// BYTES (4 or 8) of them, zeros for the rest and for what is not `there`.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t shared, const void *global, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(shared), "l"(global),
+               "n"(BYTES), "r"(there ? BYTES : 0)
+               : "memory");
+}
+// Whether pieces of elements of ES bytes can be copied ahead: a copy moves four
+// bytes at least.
+template <int ES, int A>
+constexpr bool kCopied = A == kWhole || A == kHalves || ES == 4;
+// Copies piece c of a row of H elements of ES bytes, in_row, to a 16-byte slot.
+template <int ES, int A>
+__device__ __forceinline__ void copy_piece_async(uint32_t shared, const void *row, int c, int H) {
+  static_assert(kCopied<ES, A>);
+  constexpr int N = 16 / ES;
+  const char *p = static_cast<const char *>(row) + (size_t)c * 16;
+  if constexpr (A == kWhole) {
+    copy16_async(shared, p);
+  } else if constexpr (A == kHalves) {
+    const bool there = c * N + N / 2 < H;
+    copy_async<8>(shared, p, true);
+    copy_async<8>(shared + 8, there ? p + 8 : p, there);
+  } else {
+    const char *r = static_cast<const char *>(row);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = place<N, A>(c, i);
+      copy_async<ES>(shared + i * ES, r + (size_t)(e < H ? e : 0) * ES, e < H);
+    }
+  }
+}
 // The 16 bytes at a shared-memory address.
 template <typename T>
 __device__ __forceinline__ Raw<T, kPer16<T>> raw_load_shared(uint32_t shared) {
@@ -362,6 +394,9 @@ int by_align(int align, int hidden, int bytes, F &&f) {
   if (hidden * bytes % (MIXED ? 16 : 8)) return f(std::integral_constant<int, kDealt>{});
   return f(std::integral_constant<int, kElems>{});
 }
+
+// Whether by_align's choice can be copied ahead (kCopied).
+inline bool can_copy(int align, int bytes) { return align >= kHalves || bytes == 4; }
 
 // Whether p is aligned to its elements.
 inline bool elem_aligned(const void *p, int bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
