@@ -430,8 +430,8 @@ __global__ void __launch_bounds__(grad_threads(CH)) rmsnorm_grad_kernel(NormGrad
     }
     const float2 dot2 = unpair(dot);
     const float mean = group_sum(dot2.x + dot2.y, red[turn]) * a.inv_H;
-    // dx = rstd * g + dsum - s * (rstd^2 * mean)
-    const float back = -(rstd * rstd * mean);
+    // no product of two rstd, which leaves fp32's range long before dx does
+    const f32x2 back = pair(-mean, -mean);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       if (!feed.on(i)) continue;
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(grad_threads(CH)) rmsnorm_grad_kernel(NormGrad
       weights.get(w, H, i, wf);
 #pragma unroll
       for (int e = 0; e < N / 2; ++e)
-        v[e] = fma2(s[e], pair(back, back), fma2(rstd2, mul2(d[e], wf[e]), v[e]));
+        v[e] = fma2(rstd2, fma2(mul2(s[e], rstd2), back, mul2(d[e], wf[e])), v[e]);
       raw_store<T, N, A>(static_cast<TB *>(a.dx) + out_at, tid + i * tpr, H, raw_down<T>(v));
     }
     // the slots of this row have been read: the row `depth` turns on goes there

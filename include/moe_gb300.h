@@ -566,7 +566,8 @@ size_t moe_add_rmsnorm_backward_workspace_bytes(int M, int hidden);
  *   dweight = sum over rows of dout * xh      (fp32, a fixed order)
  * dx is the gradient of x and of residual alike.  dsum, the gradient that
  * reaches sum_out from elsewhere (the residual stream), may be NULL; dweight
- * may be NULL (then no workspace is used).  M = 0 is valid: dweight = 0.
+ * may be NULL (then no workspace is used).  M = 0 is valid: dweight = 0.  A
+ * row's sum of |g * xh| must stay finite in fp32.
  *   dout, sum, dsum: M rows, *_stride apart, of type dtype; weight [hidden];
  *   rstd [M]; dx out [M][hidden], which may be dout's, sum's or dsum's own
  *   buffer when that input is dense; dweight out [hidden] float.

@@ -989,3 +989,41 @@ def test_router_gradient_behind_a_frozen_layer(shape, path):
         back = moe.moe_combine(v["y"], w, v, out_dtype=BF)
         assert int((bits(back).view(torch.int16).int() - bits(out).view(torch.int16).int())
                    .abs().max()) <= 1
+
+
+# --------------------------------------------------------------------------
+# the norm at the ends of fp32's range
+# --------------------------------------------------------------------------
+
+def walk_err(M):
+    """Roundings of a weight gradient's sum: xh; a group's rows one after the
+    other (152 CTAs of 1 to 24 groups); the groups; five parts a thread; five
+    levels of a butterfly."""
+    rows = -(-M // 152)
+    return max(rows + 1, -(-rows // 24) + 24) + 11
+
+
+@pytest.mark.parametrize("scale,gscale", [(1e-20, 1.0), (3e-20, 1.0), (1e-30, 1e-3), (1e18, 1e-3),
+                                          (1e30, 1e-3)])
+@pytest.mark.parametrize("H", [77, 520, 4100])
+@pytest.mark.parametrize("dt", [BF, FL], ids=_shape_id)
+def test_norm_gradient_of_tiny_and_huge_rows(dt, H, scale, gscale):
+    """Rows whose rstd squared, or its product with the mean, leaves fp32's
+    range; elements that are zero among them."""
+    M = 6
+    g = gen(1600 + H)
+    s, d = randn(g, M, H, dtype=dt, scale=scale), randn(g, M, H, dtype=dt, scale=gscale)
+    s[1, 5] = 0
+    w = (1 + randn(g, H, scale=0.2)).to(dt)
+    rstd = (1 / torch.sqrt(s.double().square().mean(1))).float()
+    r64 = rstd.double()[:, None]
+    xh, gw = s.double() * r64, d.double() * w.double()
+    mean = (gw * xh).mean(1, keepdim=True)
+    mag = r64 * (gw.abs() + xh.abs() * (gw * xh).abs().mean(1, keepdim=True))
+    ref = r64 * (gw - xh * mean)
+    for dsum in (None, (randn(g, M, H) * float(mag.mean())).to(dt)):
+        extra = 0 if dsum is None else dsum.double()
+        dx, dw = moe.moe_add_rmsnorm_backward(d, s, w, rstd, dsum=dsum)
+        close(dx, ref + extra, mag + (0 if dsum is None else extra.abs()), 64 * U)
+        v = d.double() * xh
+        close(dw, v.sum(0), v.abs().sum(0), walk_err(M) * U)
