@@ -207,6 +207,17 @@ struct Weights {
 // (1.07 GB) 167 us, 6.4 TB/s; with E4M3 output at M = 4096 (118 MB) 22.9 us,
 // 5.2 TB/s, of which launch, first loads and the last rows take about 4.
 
+// The sum of squares is kept in fp32, whose range it can leave while rstd does
+// not.  Where mean + eps is below 2^-80 (squares lose bits under 2^-126; they
+// are lost against eps otherwise) or overflows, a row is summed again times a
+// power of two, which comes out of the root exactly: 2^90 takes a sum of squares
+// below 2^-66 (16384 elements) to 2^114 at most, and the least element, 2^-149,
+// to 2^-59, whose square is normal; 2^-80 takes the largest, 2^128, to 2^48, and
+// 16384 of those squares are 2^110.  The test costs an ordinary row 0.2 us in 23
+// (bf16 with E4M3 output at M = 4096, hidden = 4096), nothing at M = 32768.
+constexpr float kMeanLow = 0x1p-80f, kMeanHigh = 3.402823466e38f;
+constexpr float kScaleUp = 0x1p90f, kScaleDown = 0x1p-80f;
+
 struct NormArgs {
   const void *x, *r, *w;
   int64_t xs, rs;
@@ -274,11 +285,28 @@ __global__ void __launch_bounds__(CH <= 2 ? 448 : 512, CH <= 2 ? 2 : 1)
       for (int e = 0; e < N / 2; ++e) sq = fma2(f[e], f[e], sq);
     }
     const float2 sq2 = unpair(sq);
-    const float ms = group_sum(sq2.x + sq2.y, red[turn]) * a.inv_H;
+    const float mean = group_sum(sq2.x + sq2.y, red[turn]) * a.inv_H + a.eps;
     // the slots of this row have been read: the row `depth` turns on goes there
     feed.start(row + a.depth * step, row + a.depth * step < a.M);
     turn ^= 1;
-    const float rstd = 1.f / sqrtf(ms + a.eps);
+    float rstd = 1.f / sqrtf(mean);
+    if (!(mean >= kMeanLow && mean <= kMeanHigh)) {   // the same for a whole group
+      const float c = mean < kMeanLow ? kScaleUp : kScaleDown;
+      sq = 0;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        f32x2 f[N / 2];
+        raw_up<T, N>(sr[i], f);
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) {
+          f[e] = mul2(f[e], pair(c, c));
+          sq = fma2(f[e], f[e], sq);
+        }
+      }
+      const float2 q = unpair(sq);
+      rstd = c / sqrtf(group_sum(q.x + q.y, red[turn]) * a.inv_H + a.eps * c * c);
+      turn ^= 1;
+    }
     if (a.rstd && tid == 0) a.rstd[row] = rstd;
     if (!a.out && !a.codes) continue;
 #pragma unroll

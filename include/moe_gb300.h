@@ -535,8 +535,10 @@ int moe_topk_softmax_backward(const int32_t *topk_ids, const float *topk_w,
  * shorter), from the unrounded v = s * rstd * weight:
  *   out_scale = max(max|v| / 448, 2^-126),  out_codes = e4m3(v / out_scale)
  * rounded to nearest, ties to even, and saturated; a block with a NaN gets a
- * NaN scale.  The squares' mean and the products |s * weight| * 448 must stay
- * finite in fp32.
+ * NaN scale.  The squares and their sum may leave fp32's range: rstd is right
+ * wherever it is a normal float itself.  For the codes the products
+ * |s * weight| * 448 must stay finite in fp32, and a block's largest
+ * |s * weight| zero or a normal number.
  * Types: rows BF16, F16 or F32; weight of the rows' type or F32.
  *   x, residual: M rows, *_stride apart; weight [hidden]; sum_out, out
  *   [M][hidden]; out_codes [M][hidden] bytes with out_scale

@@ -1027,3 +1027,33 @@ def test_norm_gradient_of_tiny_and_huge_rows(dt, H, scale, gscale):
         close(dx, ref + extra, mag + (0 if dsum is None else extra.abs()), 64 * U)
         v = d.double() * xh
         close(dw, v.sum(0), v.abs().sum(0), walk_err(M) * U)
+
+
+@pytest.mark.parametrize("H", [64, 300, 1111, 4096, 12340, 16384])
+@pytest.mark.parametrize("dt", [BF, FL], ids=_shape_id)
+def test_norm_of_rows_whose_squares_leave_the_range(dt, H):
+    """Squares that overflow or vanish in fp32, or whose sum does, with eps 0
+    and others; ordinary rows between them keep their bits."""
+    w = (1 + randn(gen(1700), H, scale=0.2)).to(dt)
+    scales = [1.0, 1e-12, 1e-20, 1e-23, 1e-30, 2.0 ** 62, 1.5 * 2.0 ** 63, 1e25, 1e30, 3.0, 1e19]
+    M = len(scales)
+    x = randn(gen(1701 + H), M, H, dtype=dt)
+    x = (x.double() * torch.tensor(scales, device="cuda", dtype=torch.float64)[:, None]).to(dt)
+    x[5] = 2.0 ** 62   # mean 2^124, but the sum of 4096 squares is 2^136
+    every = ("out", "sum", "rstd", "codes", "scale")
+    for eps in (0.0, 1e-6, 1e-37):
+        o = moe.moe_add_rmsnorm(x, w, eps, want=every)
+        s, rstd, p, v = norm_ref(x, None, w, eps)
+        assert ((o["rstd"].double() - rstd).abs() <= 32 * U * rstd).all()
+        close(o["out"], v, v.abs(), 36 * U)
+        check_codes(o["codes"], o["scale"], p, rstd, dt)
+        for i in (0, 9):
+            q = moe.moe_add_rmsnorm(x[i: i + 1], w, eps, want=every)
+            for name in every:
+                assert torch.equal(bits(q[name]), bits(o[name][i: i + 1])), (name, i)
+    # no size at all, and rows that are not finite, with eps 0
+    z = torch.zeros(3, H, dtype=dt, device="cuda")
+    z[1, 3], z[2, 3] = float("inf"), float("nan")
+    o = moe.moe_add_rmsnorm(z, w, 0.0, want=("rstd", "out"))
+    assert float(o["rstd"][0]) == math.inf and float(o["rstd"][1]) == 0
+    assert torch.isnan(o["rstd"][2]) and torch.isnan(o["out"][2]).all()
