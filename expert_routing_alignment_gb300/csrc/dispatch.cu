@@ -429,6 +429,9 @@ int slot_args(SlotArgs *a, int M, int top_k, int hidden, int num_rows,
   if (hidden > MOE_MAX_ROW_HIDDEN || top_k > kMaxK || (int64_t)M * top_k > MOE_MAX_SLOTS)
     return MOE_EUNSUPPORTED;
   if (M > 0 && !token_to_perm) return MOE_EINVAL;
+  if (!elem_aligned(token_to_perm, 4) || !elem_aligned(sorted_token_ids, 4) ||
+      !elem_aligned(num_tokens_post_padded, 4) || !elem_aligned(err_word, 4))
+    return MOE_EINVAL;
   *a = SlotArgs{token_to_perm, sorted_token_ids, num_tokens_post_padded, M, top_k, num_rows,
                 err_word};
   return MOE_OK;
@@ -466,7 +469,8 @@ int combine(const void *rows, int rows_dtype, const float *topk_w, const int32_t
   if (st) return st;
   const int rb = dtype_bytes(rows_dtype), ob = dtype_bytes(out_dtype);
   if ((M > 0 && !out) || (num_rows > 0 && !rows)) return MOE_EINVAL;
-  if (!elem_aligned(rows, rb) || !elem_aligned(out, ob)) return MOE_EINVAL;
+  if (!elem_aligned(rows, rb) || !elem_aligned(out, ob) || !elem_aligned(topk_w, 4))
+    return MOE_EINVAL;
   const int align = pair_alignment(rows_alignment(rows, hidden, hidden, rb),
                                    rows_alignment(out, hidden, hidden, ob), rb, ob);
   return with_types(rows_dtype, out_dtype, [&](auto R, auto O) {
@@ -565,9 +569,11 @@ extern "C" int moe_combine_backward(const void *dout, int64_t dout_stride, int o
   const int rb = dtype_bytes(rows_dtype), ob = dtype_bytes(out_dtype);
   if (!drows && !dtopk_w && M > 0) return MOE_EINVAL;
   if (M > 0 && !dout) return MOE_EINVAL;
-  if (M > 0 && num_rows > 0 && ((drows && !topk_w) || (dtopk_w && !rows))) return MOE_EINVAL;
+  // the weights of every slot are read, those of skipped ones too
+  if (M > 0 && ((drows && !topk_w) || (num_rows > 0 && dtopk_w && !rows))) return MOE_EINVAL;
   if (drows && num_rows > 0 && (!sorted_token_ids || !num_tokens_post_padded)) return MOE_EINVAL;
-  if (!elem_aligned(dout, ob) || !elem_aligned(rows, rb) || !elem_aligned(drows, rb))
+  if (!elem_aligned(dout, ob) || !elem_aligned(rows, rb) || !elem_aligned(drows, rb) ||
+      !elem_aligned(topk_w, 4) || !elem_aligned(dtopk_w, 4))
     return MOE_EINVAL;
   const int ar = rows_alignment(rows, hidden, hidden, rb);
   const int ag = rows_alignment(drows, hidden, hidden, rb);

@@ -79,7 +79,8 @@ extern "C" int moe_topk_softmax_backward(const int32_t *topk_ids, const float *t
   if (num_experts > MOE_MAX_EXPERTS || top_k > 32) return MOE_EUNSUPPORTED;
   if (M == 0) return MOE_OK;
   if (!topk_ids || !topk_w || !dtopk_w || !dlogits) return MOE_EINVAL;
-  if (((uintptr_t)topk_ids | (uintptr_t)topk_w | (uintptr_t)dtopk_w | (uintptr_t)dlogits) & 3)
+  if (((uintptr_t)topk_ids | (uintptr_t)topk_w | (uintptr_t)dtopk_w | (uintptr_t)dlogits |
+       (uintptr_t)err_word) & 3)
     return MOE_EINVAL;
   using namespace moe;
   int lanes = 1;

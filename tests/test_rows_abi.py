@@ -355,3 +355,35 @@ def test_binding_refuses_tensors_off_the_device():
         moe.moe_dispatch(x, t, K)
     with pytest.raises(ValueError, match="CUDA"):
         moe.moe_add_rmsnorm(x, torch.zeros(H, dtype=torch.bfloat16))
+
+
+# every table, weight and error word at an odd address and at an even one that
+# is not theirs; and the weights' absence where there is no row at all
+HALF = ctypes.c_void_p(4096 + 2)
+MISPLACED = [
+    ("moe_dispatch", DISPATCH, ("token_to_perm", "sorted_token_ids", "num_tokens_post_padded",
+                                "err_word")),
+    ("moe_dispatch_backward", DISPATCH_BWD, ("token_to_perm", "err_word")),
+    ("moe_combine", COMBINE, ("topk_w", "token_to_perm", "err_word")),
+    ("moe_combine_backward", COMBINE_BWD, ("topk_w", "token_to_perm", "sorted_token_ids",
+                                           "num_tokens_post_padded", "dtopk_w", "err_word")),
+    ("moe_topk_softmax_backward", TOPK_BWD, ("topk_ids", "topk_w", "dtopk_w", "dlogits",
+                                             "err_word")),
+    ("moe_add_rmsnorm", NORM, ("out_scale", "rstd")),
+    ("moe_add_rmsnorm_backward", NORM_BWD, ("rstd", "dweight")),
+]
+
+
+@pytest.mark.parametrize("fn,base,names", MISPLACED, ids=[m[0] for m in MISPLACED])
+def test_misplaced_tables_and_weights_are_refused(fn, base, names):
+    for name in names:
+        for at in (ODD, HALF):
+            assert call(fn, base, **{name: at}) == EINVAL, (name, at)
+
+
+def test_combine_gradient_wants_its_weights_whatever_the_rows():
+    """Every slot's weight is read for drows, with num_rows = 0 too."""
+    for n in (0, 64):
+        assert call("moe_combine_backward", COMBINE_BWD, topk_w=None, num_rows=n) == EINVAL
+        assert call("moe_combine_backward", COMBINE_BWD, topk_w=None, dtopk_w=None,
+                    num_rows=n) == EINVAL
