@@ -32,7 +32,8 @@ int ensure_smem_limit(const void *func, size_t bytes);
 // and device), so that kernels meant to share an SM fit together.
 int ensure_max_carveout(const void *func);
 
-// Streaming-multiprocessor count of the current device (cached per device).
+// Streaming-multiprocessor count of the current device (cached per device); 0:
+// no device, with the error recorded.
 int sm_count();
 
 // Launch with programmatic dependent launch enabled: the kernel may be

@@ -359,7 +359,9 @@ int launch_combine(const SlotArgs &a, const void *rows, const float *w, int H, v
   // at M = 4000, top_k = 6, hidden = 2880 with three of four slots skipped
   // 23.4 us with one token a CTA and 13.9 with five; at M = 4096, top_k = 8,
   // hidden = 7168 with none skipped 87.2 with one and 85.2 with four.
-  const int64_t room = (int64_t)a.M * s.parts / (8 * sm_count());
+  const int sms = sm_count();
+  if (!sms) return MOE_ECUDA;
+  const int64_t room = (int64_t)a.M * s.parts / (8 * sms);
   const int fit = 32 / a.k < 8 ? 32 / a.k : 8;
   const int tok = room < 1 ? 1 : room < fit ? (int)room : fit;
   const dim3 grid((unsigned)ceil_div64(a.M, tok), s.parts), block(s.threads);

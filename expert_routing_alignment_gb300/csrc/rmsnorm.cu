@@ -622,7 +622,9 @@ extern "C" int moe_add_rmsnorm(const void *x, int64_t x_stride, const void *resi
   const Split s = split_row(hidden, n, kTwoForward);
   const int rows = s.tpr >= 256 ? 1 : 256 / s.tpr;
   const int resident = (s.ch <= 2 ? 896 : 512) / (s.tpr * rows);
-  const int64_t turns = ceil_div64(M, rows), most = (int64_t)sm_count() * resident;
+  const int sms = sm_count();
+  if (!sms) return MOE_ECUDA;
+  const int64_t turns = ceil_div64(M, rows), most = (int64_t)sms * resident;
   const int64_t ctas = turns < most ? turns : most;
   // 64 KB in flight an SM: at M = 32768, hidden = 4096 in bf16 162 us, but
   // 192 us with 128 KB (the reads crowd out the writes)

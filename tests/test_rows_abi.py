@@ -7,6 +7,8 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -387,3 +389,31 @@ def test_combine_gradient_wants_its_weights_whatever_the_rows():
         assert call("moe_combine_backward", COMBINE_BWD, topk_w=None, num_rows=n) == EINVAL
         assert call("moe_combine_backward", COMBINE_BWD, topk_w=None, dtopk_w=None,
                     num_rows=n) == EINVAL
+
+
+NO_DEVICE = """
+import ctypes
+import expert_routing_alignment_gb300 as moe
+from tests import test_rows_abi as t
+for fn, base in (("moe_dispatch", t.DISPATCH), ("moe_dispatch_backward", t.DISPATCH_BWD),
+                 ("moe_combine", t.COMBINE), ("moe_combine_backward", t.COMBINE_BWD),
+                 ("moe_topk_softmax_backward", t.TOPK_BWD), ("moe_add_rmsnorm", t.NORM),
+                 ("moe_add_rmsnorm_backward", t.NORM_BWD)):
+    assert t.call(fn, base) == moe.MOE_ECUDA, fn
+    assert moe.load().moe_last_cuda_error() != 0, fn
+layer = t._layer()
+a, b, c, d = (ctypes.c_void_p(4096 * i) for i in (2, 3, 4, 5))
+assert moe.load().moe_decode_block(
+    ctypes.pointer(layer._struct), a, b, t.F, 1e-6, 4, b, c, d, ctypes.c_void_p(1 << 20),
+    moe.workspace_bytes(layer, 4), None, None) == moe.MOE_ECUDA
+print("refused")
+"""
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="its pointers are no device buffers")
+def test_without_a_device_every_call_returns_its_error():
+    """In a process of its own, with every device hidden: a call that fails to
+    find one must not end the process."""
+    p = subprocess.run([sys.executable, "-c", NO_DEVICE], capture_output=True, text=True, cwd=ROOT,
+                       env={**os.environ, "CUDA_VISIBLE_DEVICES": ""}, timeout=300)
+    assert p.returncode == 0 and "refused" in p.stdout, (p.returncode, p.stderr[-2000:])
