@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(256) dispatch_kernel(SlotArgs a, const char *x
     if (blockIdx.y == 0)
       for (int i = tid; i < n / a.k * scales; i += blockDim.x) {
         const int t = i / scales, col = i - t * scales;
-        const float q = __ldg(xs + (t0 + t) * scales + col);
+        const float q = xs[(t0 + t) * scales + col];
         for (int j = 0; j < a.k; ++j)
           if (pos[t * a.k + j] >= 0) rs[(size_t)pos[t * a.k + j] * scales + col] = q;
       }

@@ -197,7 +197,9 @@ __device__ __forceinline__ void store16(void *row, int c, int H, const uint4 &q)
 
 // Piece c (N elements, 16 bytes, or 8 in the 16-bit type of a mixed pair) of a
 // row of H elements, in_row; zeros behind the end.  Plain (coherent) loads: some
-// callers let an output share an input's buffer.
+// callers let an output share an input's buffer, and under programmatic launch
+// the grid in front may still write these rows when this one becomes resident
+// (no ld.global.nc, which asks for data that is read-only for a grid's life).
 template <typename T, int N, int A>
 __device__ __forceinline__ Raw<T, N> raw_load(const typename T::bits *row, int c, int H) {
   constexpr int ES = sizeof(typename T::bits);

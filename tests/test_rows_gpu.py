@@ -1057,3 +1057,41 @@ def test_norm_of_rows_whose_squares_leave_the_range(dt, H):
     o = moe.moe_add_rmsnorm(z, w, 0.0, want=("rstd", "out"))
     assert float(o["rstd"][0]) == math.inf and float(o["rstd"][1]) == 0
     assert torch.isnan(o["rstd"][2]) and torch.isnan(o["out"][2]).all()
+
+
+def test_codes_and_scales_reach_expert_order_in_one_stream():
+    """The norm's E4M3 rows and scales dispatched by the call right behind it,
+    eagerly, replayed, and over new inputs in the same buffers: the dispatch
+    may be resident while the norm still writes them."""
+    M, H, k, E = 700, 2048, 4, 16
+    _, _, t = route(M, E, k, 16, 1800)
+    perm, total = perm_of(t, M, k), int(t["num_tokens_post_padded"])
+    x, r, w = norm_inputs(M, H, BF, BF, 1801)
+    o = moe.alloc_add_rmsnorm_outputs(x, ("codes", "scale"))
+    rows = torch.empty(t["max_total"], H, dtype=E4, device="cuda")
+    scale = torch.empty(t["max_total"], H // 128, device="cuda")
+
+    def both():
+        moe.moe_add_rmsnorm(x, w, residual=r, out=o)
+        moe.moe_dispatch(o["codes"], t, k, rows=rows, x_scale=o["scale"], rows_scale=scale)
+
+    def check():
+        torch.cuda.synchronize()
+        s, rstd, p, _ = norm_ref(x, r, w, 1e-6)
+        check_codes(o["codes"], o["scale"], p, rstd, BF)
+        for got, src in ((rows, o["codes"]), (scale, o["scale"])):
+            assert torch.equal(bits(got[perm]), bits(src[:, None].expand(M, k, -1)))
+        pad, _ = padding(t, M * k)
+        assert not bits(rows[pad]).any() and not scale[:total][pad[:total]].any()
+    both()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+        both()
+    for seed in range(4):
+        a, b, _ = norm_inputs(M, H, BF, BF, 1810 + seed)
+        x.copy_(a)
+        r.copy_(b)
+        graph.replay()
+        check()
