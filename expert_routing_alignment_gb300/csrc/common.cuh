@@ -61,29 +61,36 @@ int launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
   return MOE_OK;
 }
 
-// launch_pdl for a grid whose CTAs wait on one another: also cooperative, so
-// the launch fails unless every CTA can be resident at once.
+// Launch of a grid whose CTAs wait on one another: cooperative, so the launch
+// fails unless every CTA can be resident at once.  pdl: as launch_pdl, else it
+// starts once its predecessor has finished.
 template <typename... KArgs, typename... Args>
-int launch_pdl_coop(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                    void *stream, Args... args) {
+int launch_coop(bool pdl, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                void *stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeCooperative;
-  attr[1].val.cooperative = 1;
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = pdl ? 2 : 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ((KArgs)args)...);
   if (e != cudaSuccess) {
     set_last_cuda_error(e);
     return MOE_ECUDA;
   }
   return MOE_OK;
+}
+
+template <typename... KArgs, typename... Args>
+int launch_pdl_coop(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, void *stream,
+                    Args... args) {
+  return launch_coop(true, kernel, grid, block, smem, stream, args...);
 }
 
 inline int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -170,6 +177,9 @@ __device__ __forceinline__ float e4m3_to_float(uint32_t byte) {
 __device__ __forceinline__ float silu_f32(float z) { return z / (1.0f + expf(-z)); }
 
 // Loads that bypass L1 for data written by an earlier kernel of the stream.
+// (Where L1 helps, plain loads; never __ldg, which is for weights: it asks for
+// data that nothing writes while the grid is resident, and a grid may be
+// resident before its predecessor has finished.)
 __device__ __forceinline__ int ld_cg(const int32_t *p) { return __ldcg(p); }
 
 // 16-byte streaming load of read-only weights (not kept in L1).

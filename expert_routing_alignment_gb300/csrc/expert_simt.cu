@@ -230,7 +230,7 @@ __device__ __forceinline__ void gate_up_item(const ExpertsDev &X, int e, int o_b
       const int r = idx / (H / 8);
       const int k = (idx % (H / 8)) * 8;
       const int tok = row_slots ? __ldcg(row_slots + r0 + r) / top_k : r0 + r;
-      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(x + (size_t)tok * H + k));
+      const uint4 v = *reinterpret_cast<const uint4 *>(x + (size_t)tok * H + k);
       float *dst = xs_smem + (size_t)r * H;
       // k is a multiple of 8: two whole quads of the interleaved layout
       *reinterpret_cast<float4 *>(dst + xs_index<FMT>(k, nch)) =

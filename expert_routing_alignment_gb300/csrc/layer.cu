@@ -26,7 +26,7 @@ void tc_workspace(const moe_layer_desc *L, int M, int max_total, int cap, size_t
 size_t tc_counter_ints(const moe_layer_desc *L);
 int launch_tc(const moe_layer_desc *L, const uint16_t *x, int M, const float *w,
               const int32_t *ttp, const int32_t *act_count, uint16_t *out, void *ws,
-              const moe_workspace_view &v, uint32_t *err, void *stream);
+              const moe_workspace_view &v, bool x_final, uint32_t *err, void *stream);
 int align_launch(const void *topk_ids, int ids_is_int64, int n, int num_experts, int block_size,
                  int32_t *sorted_token_ids, int32_t *sorted_expert_ids, int32_t *expert_offsets,
                  int32_t *token_to_perm, int32_t *active_experts, int32_t *active_count,
@@ -45,7 +45,7 @@ int launch_fused(const moe_layer_desc *L, const uint16_t *x, int M, const float 
 
 int run_experts(const moe_layer_desc *layer, int run, const uint16_t *x, int M,
                 const int32_t *ids, const float *w, uint16_t *out, void *workspace,
-                const moe_workspace_view &v, uint32_t *err_word, void *stream);
+                const moe_workspace_view &v, bool x_final, uint32_t *err_word, void *stream);
 
 // The expert-kernel path of the grouped entry points.  The tensor-core
 // kernels keep their activation terms in the layer workspace, so only
@@ -319,17 +319,17 @@ extern "C" int moe_decode_layer(const moe_layer_desc *layer, const uint16_t *x, 
                          moe::is_tc(run) ? reinterpret_cast<int4 *>(ws + v.tc_items) : nullptr,
                          &xp, stream);
   if (st) return st;
-  return moe::run_experts(layer, run, x, M, ids, w, out, workspace, v, err_word, stream);
+  return moe::run_experts(layer, run, x, M, ids, w, out, workspace, v, true, err_word, stream);
 }
 
 namespace moe {
 
 // The expert half of a layer call, after the routing and the alignment
 // tables are in the workspace: a tensor-core kernel, or the staged gate+up,
-// down and blend.
+// down and blend.  x_final: launch_tc's.
 int run_experts(const moe_layer_desc *layer, int run, const uint16_t *x, int M,
                 const int32_t *ids, const float *w, uint16_t *out, void *workspace,
-                const moe_workspace_view &v, uint32_t *err_word, void *stream) {
+                const moe_workspace_view &v, bool x_final, uint32_t *err_word, void *stream) {
   char *ws = reinterpret_cast<char *>(workspace);
   auto I32 = [&](size_t o) { return reinterpret_cast<int32_t *>(ws + o); };
   auto F32 = [&](size_t o) { return reinterpret_cast<float *>(ws + o); };
@@ -338,7 +338,7 @@ int run_experts(const moe_layer_desc *layer, int run, const uint16_t *x, int M,
   (void)ids;
   if (run == kRunTc)
     return launch_tc(layer, x, M, w, I32(v.token_to_perm), I32(v.active_count), out, workspace,
-                     v, err_word, stream);
+                     v, x_final, err_word, stream);
   if (run == kRunTcF4)
     return launch_f4(layer, x, M, w, I32(v.token_to_perm), I32(v.active_count), out, workspace,
                      v, err_word, stream);
@@ -375,5 +375,6 @@ extern "C" int moe_decode_experts(const moe_layer_desc *layer, const uint16_t *x
   // the tensor-core runs' per-token x table of this x (one launch more)
   st = moe::xprep_launch(moe::token_table(layer, run, x, M, ws, v), stream);
   if (st) return st;
-  return moe::run_experts(layer, run, x, M, ids, w, out, workspace, v, err_word, stream);
+  // x may come from the call ahead
+  return moe::run_experts(layer, run, x, M, ids, w, out, workspace, v, false, err_word, stream);
 }

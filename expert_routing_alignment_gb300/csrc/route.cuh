@@ -87,7 +87,7 @@ __device__ __forceinline__ float shared_gate_warp(const uint16_t *x, const uint1
   float z = 0.f;
 #pragma unroll 4
   for (int c = lane; c < H / 8; c += 32) {
-    const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(x) + c);
+    const uint4 xv = reinterpret_cast<const uint4 *>(x)[c];
     const uint4 gv = __ldg(reinterpret_cast<const uint4 *>(g) + c);
     const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w}, gs[4] = {gv.x, gv.y, gv.z, gv.w};
 #pragma unroll

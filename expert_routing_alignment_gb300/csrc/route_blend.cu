@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kRouterThreads)
 #pragma unroll
       for (int r = 0; r < kRouterRows; ++r)
         xv[u][r] = c < chunks && t0 + r < M
-                       ? __ldg(reinterpret_cast<const uint4 *>(x + (size_t)(t0 + r) * H) + c)
+                       ? reinterpret_cast<const uint4 *>(x + (size_t)(t0 + r) * H)[c]
                        : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll

@@ -46,7 +46,7 @@ __device__ inline void xprep_token(const XPrep &p, int t, int *red) {
   float dot = 0.f;
   const bool gated = p.mode == kXPrepF16 && p.gate_w;
   for (int c = tid * 8; worker && c < p.H; c += kXPrepThreads * 8) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(xr + c));
+    const uint4 v = *reinterpret_cast<const uint4 *>(xr + c);
     const uint32_t xv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
@@ -96,26 +96,45 @@ __device__ inline void xprep_token(const XPrep &p, int t, int *red) {
     }
   }
   if (!worker) return;
+  // loads in batches ahead of the stores they might alias
   if (p.mode == kXPrepE4M3) {
-    for (int c = tid * 4; c < p.H; c += kXPrepThreads * 4) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(xr + c));
-      uint32_t t0a, t1a, t0b, t1b;
-      e4m3_split2(bf16_to_float((uint16_t)(v.x & 0xFFFFu)) * scl,
-                  bf16_to_float((uint16_t)(v.x >> 16)) * scl, t0a, t1a);
-      e4m3_split2(bf16_to_float((uint16_t)(v.y & 0xFFFFu)) * scl,
-                  bf16_to_float((uint16_t)(v.y >> 16)) * scl, t0b, t1b);
-      uint8_t *dst = p.table + (size_t)(c / 128) * 2 * 16 * 128 + (size_t)t * 128 + c % 128;
-      *reinterpret_cast<uint32_t *>(dst) = t0a | (t0b << 16);
-      *reinterpret_cast<uint32_t *>(dst + 16 * 128) = t1a | (t1b << 16);
+    constexpr int S = kXPrepThreads * 4;
+    for (int c0 = tid * 4; c0 < p.H; c0 += 4 * S) {
+      uint2 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (c0 + u * S < p.H) v[u] = *reinterpret_cast<const uint2 *>(xr + c0 + u * S);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int c = c0 + u * S;
+        if (c >= p.H) break;
+        uint32_t t0a, t1a, t0b, t1b;
+        e4m3_split2(bf16_to_float((uint16_t)(v[u].x & 0xFFFFu)) * scl,
+                    bf16_to_float((uint16_t)(v[u].x >> 16)) * scl, t0a, t1a);
+        e4m3_split2(bf16_to_float((uint16_t)(v[u].y & 0xFFFFu)) * scl,
+                    bf16_to_float((uint16_t)(v[u].y >> 16)) * scl, t0b, t1b);
+        uint8_t *dst = p.table + (size_t)(c / 128) * 2 * 16 * 128 + (size_t)t * 128 + c % 128;
+        *reinterpret_cast<uint32_t *>(dst) = t0a | (t0b << 16);
+        *reinterpret_cast<uint32_t *>(dst + 16 * 128) = t1a | (t1b << 16);
+      }
     }
   } else {
-    for (int c = tid * 2; c < p.H; c += kXPrepThreads * 2) {
-      const uint32_t v = __ldg(reinterpret_cast<const uint32_t *>(xr + c));
-      const uint32_t hv = f16x2_rn(bf16_to_float((uint16_t)(v & 0xFFFFu)) * scl,
-                                   bf16_to_float((uint16_t)(v >> 16)) * scl);
-      const int kb = c / 128, half = (c % 128) / 64;
-      uint8_t *dst = p.table + ((size_t)(kb * 2 + half) * p.NT + t) * 128 + (c % 64) * 2;
-      *reinterpret_cast<uint32_t *>(dst) = hv;
+    constexpr int S = kXPrepThreads * 2;
+    for (int c0 = tid * 2; c0 < p.H; c0 += 8 * S) {
+      uint32_t v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (c0 + u * S < p.H) v[u] = *reinterpret_cast<const uint32_t *>(xr + c0 + u * S);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int c = c0 + u * S;
+        if (c >= p.H) break;
+        const uint32_t hv = f16x2_rn(bf16_to_float((uint16_t)(v[u] & 0xFFFFu)) * scl,
+                                     bf16_to_float((uint16_t)(v[u] >> 16)) * scl);
+        const int kb = c / 128, half = (c % 128) / 64;
+        uint8_t *dst = p.table + ((size_t)(kb * 2 + half) * p.NT + t) * 128 + (c % 64) * 2;
+        *reinterpret_cast<uint32_t *>(dst) = hv;
+      }
     }
   }
 }

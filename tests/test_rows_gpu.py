@@ -1095,3 +1095,45 @@ def test_codes_and_scales_reach_expert_order_in_one_stream():
         r.copy_(b)
         graph.replay()
         check()
+
+
+@pytest.mark.parametrize("shape,path", LAYERS + [(synth.decode_fp8(32), 0)],
+                         ids=lambda v: getattr(v, "name", str(v)))
+def test_the_layers_calls_right_behind_the_norm_that_writes_their_rows(shape, path):
+    """The router, the layer and its expert half on rows that the norm in front
+    writes into the same buffer each time, replayed without a gap: the bits of
+    calls that wait for it."""
+    inp, layer = make_layer(shape, path, router=True)
+    M, H = shape.M, shape.H
+    weight = torch.ones(H, dtype=BF, device="cuda")
+    rows = [randn(gen(1900 + i), M, H, dtype=BF) for i in range(3)]
+    ws, out = moe.alloc_workspace(layer, M), torch.empty(M, H, dtype=BF, device="cuda")
+    moe.moe_decode_layer(layer, inp.x, out, ws)
+    n = torch.empty(M, H, dtype=BF, device="cuda")
+    lg = torch.empty(M, shape.E, device="cuda")
+
+    def router(o):
+        moe.moe_router_logits(n, layer.router_weight, logits=lg)
+        o.copy_(lg[:, :1])
+
+    calls = [lambda o: moe.moe_decode_experts(layer, n, o, ws),
+             lambda o: moe.moe_decode_layer(layer, n, o, ws, router_logits=inp.logits), router]
+    for call in calls:
+        want = []
+        for x in rows:
+            moe.moe_add_rmsnorm(x, weight, out=dict(out=n))
+            torch.cuda.synchronize()
+            want.append(torch.empty_like(out))
+            call(want[-1])
+            torch.cuda.synchronize()
+        got = [torch.empty_like(out) for _ in rows]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for x, o in zip(rows, got):
+                moe.moe_add_rmsnorm(x, weight, out=dict(out=n))
+                call(o)
+        for _ in range(5):
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(got, want):
+                assert torch.equal(bits(a), bits(b))
