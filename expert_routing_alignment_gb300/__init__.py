@@ -481,14 +481,14 @@ _ROWS = {**_FLOAT, torch.float8_e4m3fn: DTYPE_E4M3, torch.uint8: DTYPE_E4M3}
 # These wrappers stand in front of kernels of a few microseconds, so they pass
 # plain addresses, check each tensor once and ask for the current device and
 # stream directly (a torch.cuda.Stream object costs more than the launch).
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# torch has those two calls in a build with CUDA only, so they are looked up
+# when a device tensor needs them, not when this module is imported.
 
 
 def _on_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
     """The kernels run on the current device: refuse tensors of any other."""
     dev = first.get_device()
-    if dev < 0 or dev != _current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError(f"want CUDA tensors of the current device, got one on {first.device}")
     for t in others:
         if t is not None and t.get_device() != dev:
@@ -499,7 +499,7 @@ def _on_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
 def _handle(stream, dev: int) -> int:
     """The cudaStream_t of a stream argument; None: the device's current one."""
     if stream is None:
-        return _current_stream(dev)
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 

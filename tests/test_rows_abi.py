@@ -417,3 +417,26 @@ def test_without_a_device_every_call_returns_its_error():
     p = subprocess.run([sys.executable, "-c", NO_DEVICE], capture_output=True, text=True, cwd=ROOT,
                        env={**os.environ, "CUDA_VISIBLE_DEVICES": ""}, timeout=300)
     assert p.returncode == 0 and "refused" in p.stdout, (p.returncode, p.stderr[-2000:])
+
+
+NO_CUDA = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):   # as in a build without CUDA
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import expert_routing_alignment_gb300 as moe
+assert moe.moe_align_sizes(16, 8, 16)[0] > 0
+assert moe.add_rmsnorm_backward_workspace_bytes(4, 256) > 0
+x = torch.zeros(2, 64, dtype=torch.bfloat16)
+try:
+    moe.moe_add_rmsnorm(x, x[0])
+except ValueError as e:
+    assert "CUDA" in str(e)
+    print("refused")
+"""
+
+
+def test_import_and_host_calls_need_no_cuda_build_of_torch():
+    p = subprocess.run([sys.executable, "-c", NO_CUDA], capture_output=True, text=True, cwd=ROOT,
+                       timeout=300)
+    assert p.returncode == 0 and "refused" in p.stdout, (p.returncode, p.stderr[-2000:])
