@@ -1137,3 +1137,88 @@ def test_the_layers_calls_right_behind_the_norm_that_writes_their_rows(shape, pa
             torch.cuda.synchronize()
             for a, b in zip(got, want):
                 assert torch.equal(bits(a), bits(b))
+
+
+# --------------------------------------------------------------------------
+# walks of several rows a group, batches beyond the plans' thresholds
+# --------------------------------------------------------------------------
+
+# (M, H, type, weights' type): more rows than the groups of a full grid take at
+# once, and no whole number of turns.  Pieces a thread 1, 2, 4 and 8; rows of
+# whole pieces, of halves, and of other widths.
+WALKS = [(9001, 128, BF, BF), (4001, 2048, BF, BF), (1801, 3600, BF, FL), (2001, 12344, BF, BF),
+         (9001, 132, HF, HF), (6001, 1028, BF, BF), (3001, 2884, BF, BF), (2001, 12340, HF, FL),
+         (9001, 77, BF, BF), (3001, 513, BF, BF), (3001, 2885, HF, HF), (2001, 12345, BF, BF),
+         (3001, 512, FL, FL), (3001, 1600, FL, FL), (2001, 4096, FL, FL), (1001, 16384, FL, FL),
+         (3001, 514, FL, FL), (1001, 16382, FL, FL), (3001, 513, FL, FL), (2001, 2005, FL, FL),
+         (2001, 5001, FL, FL), (1001, 16383, FL, FL)]
+walks = pytest.mark.parametrize("M,H,dt,wt", WALKS, ids=_shape_id)
+
+
+@walks
+def test_norm_of_more_rows_than_a_grid_takes_at_once(M, H, dt, wt):
+    """Against float64, and bit for bit the rows of small batches."""
+    x, r, w = norm_inputs(M, H, dt, wt, 1300 + H)
+    every = ("out", "sum", "rstd", "codes", "scale")
+    o = moe.moe_add_rmsnorm(x, w, residual=r, want=every)
+    s, rstd, p, v = norm_ref(x, r, w, 1e-6)
+    assert torch.equal(o["sum"].double(), s)
+    assert ((o["rstd"].double() - rstd).abs() <= 32 * U * rstd).all()
+    close(o["out"], v, v.abs(), 36 * U)
+    check_codes(o["codes"], o["scale"], p, rstd, dt if wt != FL else FL)
+    for at in range(0, M, 150):
+        b = slice(at, min(at + 150, M))
+        q = moe.moe_add_rmsnorm(x[b], w, residual=r[b], want=every)
+        for name in every:
+            assert torch.equal(bits(q[name]), bits(o[name][b])), (name, at)
+
+
+@walks
+def test_norm_gradient_of_more_rows_than_a_grid_takes_at_once(M, H, dt, wt):
+    x, s, w = norm_inputs(M, H, dt, wt, 1400 + H)
+    dsum = randn(gen(1401), M, H, dtype=dt)
+    rstd = (1 / torch.sqrt(s.double().square().mean(1) + 1e-6)).float()
+    r64 = rstd.double()[:, None]
+    d, xh = x.double(), s.double() * r64
+    gw = d * w.double()
+    mean = (gw * xh).mean(1, keepdim=True)
+    dx, dw = moe.moe_add_rmsnorm_backward(x, s, w, rstd, dsum=dsum)
+    mag = r64 * (gw.abs() + xh.abs() * (gw * xh).abs().mean(1, keepdim=True)) + dsum.double().abs()
+    close(dx, r64 * (gw - xh * mean) + dsum.double(), mag, 64 * U)
+    v = d * xh
+    close(dw, v.sum(0), v.abs().sum(0), walk_err(M) * U)
+    plain, _ = moe.moe_add_rmsnorm_backward(x, s, w, rstd, want_dweight=False)
+    for at in range(0, M, 150):
+        b = slice(at, min(at + 150, M))
+        a, _ = moe.moe_add_rmsnorm_backward(x[b], s[b], w, rstd[b], dsum=dsum[b],
+                                            want_dweight=False)
+        assert torch.equal(bits(a), bits(dx[b])), at
+        a, _ = moe.moe_add_rmsnorm_backward(x[b], s[b], w, rstd[b], want_dweight=False)
+        assert torch.equal(bits(a), bits(plain[b])), at
+
+
+@pytest.mark.parametrize("H", [1024, 1028, 1111, 2880])
+@pytest.mark.parametrize("k", [1, 2, 4, 8])
+@pytest.mark.parametrize("rt,ot", [(BF, BF), (FL, FL), (FL, BF)], ids=_shape_id)
+def test_a_tokens_bits_in_batches_of_every_plan(H, k, rt, ot):
+    """A batch whose plan takes several tokens a CTA, and its first tokens in
+    batches of one, of seven and of a thousand."""
+    M, E = 9000, 16
+    _, w, t = route(M, E, k, 16, 1500 + k, 0.2)
+    perm = perm_of(t, M, k)
+    g = gen(1501)
+    rows, dout = randn(g, t["max_total"], H, dtype=rt), randn(g, M, H, dtype=ot)
+    x = randn(g, M, H, dtype=rt)
+    out = moe.moe_combine(rows, w, t, out_dtype=ot)
+    dr, dw = moe.moe_combine_backward(dout, rows, w, t)
+    dx = moe.moe_dispatch_backward(rows, t, M, k)
+    put = moe.moe_dispatch(x, t, k)
+    for n in (1, 7, 1000):
+        sub = dict(t, token_to_perm=t["token_to_perm"][: n * k].contiguous())
+        real = perm[:n][perm[:n] >= 0]
+        a, b = moe.moe_combine_backward(dout[:n], rows, w[:n], sub)
+        for got, want in ((moe.moe_combine(rows, w[:n], sub, out_dtype=ot), out[:n]),
+                          (a[real], dr[real]), (b, dw[:n]),
+                          (moe.moe_dispatch_backward(rows, sub, n, k), dx[:n]),
+                          (moe.moe_dispatch(x[:n], sub, k)[real], put[real])):
+            assert torch.equal(bits(got), bits(want)), n
