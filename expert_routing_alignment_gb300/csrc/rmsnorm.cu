@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(CH <= 2 ? 448 : 512, CH <= 2 ? 2 : 1)
 // SM adds its groups' parts in order, the CTAs' parts go to the workspace
 // [CTAs][H] and a second kernel adds those in a fixed order, so the bits are
 // the same every time.  Bound by HBM: bf16 at M = 10007, hidden = 4096 (328 MB)
-// 54.4 us, 6.0 TB/s, of which the second kernel and its launch take about 4.
+// 53.9 us, 6.1 TB/s, of which the second kernel and its launch take about 3.
 
 struct NormGradArgs {
   const void *dout, *sum, *dsum, *w;
@@ -514,19 +514,26 @@ __global__ void __launch_bounds__(grad_threads(CH)) rmsnorm_grad_kernel(NormGrad
   }
 }
 
-// dw[h] = sum over the CTAs' parts: 32 columns a CTA, 32 threads a column that
-// take every 32nd part (eight loads in flight), then a butterfly over those.
+constexpr int kSms = 152;
+
+// dw[h] = sum over the CTAs' parts, kSms at most: 32 columns a CTA, 32 threads a
+// column that take every 32nd part (five at most, all loads ahead of the sums),
+// then a butterfly over those.
 __global__ void __launch_bounds__(1024) sum_parts_kernel(const float *part, int n, int H,
                                                          float *dw) {
   __shared__ float red[32][33];
   pdl_wait();
   pdl_trigger();
   const int x = threadIdx.x, y = threadIdx.y, h = blockIdx.x * 32 + x;
-  float v = 0.f;
-  if (h < H) {
-#pragma unroll 8
-    for (int i = y; i < n; i += 32) v += __ldcg(part + (size_t)i * H + h);
+  constexpr int kEach = (kSms + 31) / 32;
+  float q[kEach], v = 0.f;
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const int i = y + 32 * u;
+    q[u] = h < H && i < n ? __ldcg(part + (size_t)i * H + h) : 0.f;
   }
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) v += q[u];
   red[y][x] = v;
   __syncthreads();
   v = red[x][y];   // column y of the CTA, its x-th sum
@@ -534,8 +541,6 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float *part, int 
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
   if (x == 0 && blockIdx.x * 32 + y < H) dw[blockIdx.x * 32 + y] = v;
 }
-
-constexpr int kSms = 152;
 
 // The walk of the gradient over M rows: one CTA an SM (a constant, not the
 // device's count: dw's order depends on M, hidden and the type alone), as many
