@@ -229,9 +229,13 @@ __global__ void __launch_bounds__(256) combine_kernel(SlotArgs a, const typename
 // sums), the warps' sums are added in warp order.  A sum's order depends on
 // hidden and the type alone: a token's bits are the same in every batch.
 // Bound by HBM: bf16 at M = 16384, hidden = 4096, top_k = 8 (2.42 GB, half of
-// it written) 365 us, 6.6 TB/s; three CTAs an SM (80 registers), since 96
+// it written) 365 us, 6.6 TB/s; three CTAs an SM (80 registers; four tokens a CTA
+// spill 16 to 64 bytes there, 16-bit rows of whole pieces none), since 96
 // registers and two CTAs took 408 us.  Weights alone (fp32 rows, M = 512,
-// hidden = 4096: 71 MB) 14 us, 5.1 TB/s, one wave of four CTAs an SM.
+// hidden = 4096: 71 MB) 14 us, 5.1 TB/s, one wave of four CTAs an SM.  Skipped
+// slots leave their loads unissued and their CTA's time with little in flight:
+// bf16 at M = 4000, top_k = 6, hidden = 2880 with three of four skipped 38.5 us,
+// 2.6 TB/s, weights alone 27.2.
 
 template <typename R, typename O, int TOK, bool DW, bool DR, int A>
 __global__ void __launch_bounds__(256, DR ? 3 : TOK > 1 ? 3 : 4) combine_grad_kernel(
@@ -344,7 +348,9 @@ Parts split_parts(int pieces) {
 }
 
 // CTAs of a kernel that clears padding besides its tokens: with few tokens, up
-// to one for every eight positions.
+// to one for every eight positions, eight an SM at most (bf16 dispatch at
+// M = 512, hidden = 2048 over 128 experts in blocks of 64: 11.5 us with one an
+// SM, 10.7 with four, 8.6 with eight, 8.3 with sixteen, more than are resident).
 int64_t pad_ctas(int64_t ctas, int num_rows) {
   const int64_t pads = ceil_div64(num_rows, kPadRows);
   const int64_t most = 8 * (int64_t)sm_count();
@@ -358,7 +364,9 @@ int launch_combine(const SlotArgs &a, const void *rows, const float *w, int H, v
   // Up to eight tokens and 32 slots a CTA while eight CTAs an SM remain: bf16
   // at M = 4000, top_k = 6, hidden = 2880 with three of four slots skipped
   // 23.4 us with one token a CTA and 13.9 with five; at M = 4096, top_k = 8,
-  // hidden = 7168 with none skipped 87.2 with one and 85.2 with four.
+  // hidden = 7168 with none skipped 87.2 with one and 85.2 with four.  With two,
+  // four or eight CTAs an SM 13.6 and 84.8, with sixteen 14.2 and 84.8, with 32
+  // 23.1 and 85.5.
   const int sms = sm_count();
   if (!sms) return MOE_ECUDA;
   const int64_t room = (int64_t)a.M * s.parts / (8 * sms);

@@ -3,7 +3,6 @@
 // (moe_add_rmsnorm_backward).
 #include <math.h>
 
-
 #include "common.cuh"
 #include "rows.cuh"
 
@@ -204,8 +203,10 @@ struct Weights {
 // the quotient's, and the codes do not depend on the order of the sum of
 // squares.  Where the scale would be below 2^-126 it is 2^-126, so that no
 // scale is zero or subnormal.  Bound by HBM: bf16 at M = 32768, hidden = 4096
-// (1.07 GB) 167 us, 6.4 TB/s; with E4M3 output at M = 4096 (118 MB) 22.9 us,
-// 5.2 TB/s, of which launch, first loads and the last rows take about 4.
+// (1.07 GB) 165 us, 6.5 TB/s; with E4M3 output at M = 4096 (118 MB) 23.0 us,
+// 5.1 TB/s, of which launch, first loads and the last rows take about 4.  72
+// registers a thread with one or two pieces: rows of other widths spill up to 48
+// bytes there.
 
 // The sum of squares is kept in fp32, whose range it can leave while rstd does
 // not.  Where mean + eps is below 2^-80 (squares lose bits under 2^-126; they
@@ -390,8 +391,10 @@ __global__ void __launch_bounds__(CH <= 2 ? 448 : 512, CH <= 2 ? 2 : 1)
 // A group walks over its rows with their part of dw in registers; one CTA an
 // SM adds its groups' parts in order, the CTAs' parts go to the workspace
 // [CTAs][H] and a second kernel adds those in a fixed order, so the bits are
-// the same every time.  Bound by HBM: bf16 at M = 10007, hidden = 4096 (328 MB)
-// 53.9 us, 6.1 TB/s, of which the second kernel and its launch take about 3.
+// the same every time.  80 registers a thread with two pieces (8 bytes of spills
+// on whole pieces, up to 76 by elements).  Bound by HBM: bf16 at M = 10007,
+// hidden = 4096 (328 MB) 53.9 us, 6.1 TB/s, of which the second kernel and its
+// launch take about 3.
 
 struct NormGradArgs {
   const void *dout, *sum, *dsum, *w;
@@ -631,8 +634,9 @@ extern "C" int moe_add_rmsnorm(const void *x, int64_t x_stride, const void *resi
   if (!sms) return MOE_ECUDA;
   const int64_t turns = ceil_div64(M, rows), most = (int64_t)sms * resident;
   const int64_t ctas = turns < most ? turns : most;
-  // 64 KB in flight an SM: at M = 32768, hidden = 4096 in bf16 162 us, but
-  // 192 us with 128 KB (the reads crowd out the writes)
+  // 64 KB in flight an SM: at M = 32768, hidden = 4096 in bf16 165 us, but 175
+  // with 96 or 128 KB (the reads crowd out the writes); at M = 16384, hidden =
+  // 1024 23.3, with 32 KB 27.4, with 128 KB 25.6
   const size_t stage = (size_t)2 * s.ch * s.tpr * rows * 16;
   const int depth = plan_depth(stage, resident, ceil_div64(turns, ctas), 64 * 1024);
   const NormArgs a{x,   residual, weight,    x_stride,  residual_stride, M, hidden, depth,
@@ -702,6 +706,13 @@ extern "C" int moe_add_rmsnorm_backward(const void *dout, int64_t dout_stride, c
   if (M > 0) {
     const size_t stage = (size_t)3 * s.ch * s.tpr * walk.groups * 16;
     const int64_t turns = ceil_div64(M, (int64_t)walk.ctas * walk.groups);
+    // 144 KB: two stages of the widest rows that are split in two a thread (72 KB,
+    // 16-bit rows of 4096): at M = 10007 55.7 us, with one stage 64.1, with three
+    // 56.6.  Narrower rows have up to four stages, of which 72 KB would do (M =
+    // 16384, hidden = 1024: 26.7 us, with 72 KB 25.8); wider ones have one stage
+    // of up to 192 KB, and a second where it would fit
+    // gains 1 to 4 % (M = 4096, hidden = 7168 51.8 and 51.4; fp32 4096 47.6 and
+    // 45.5, but bf16 16384 60.0 and 61.1).
     const int depth = plan_depth(stage, 1, turns, 144 * 1024);
     const size_t ring = can_copy(align, b) ? depth * stage : 0;
     const size_t parts = walk.groups > 1 ? (size_t)walk.groups * hidden * sizeof(float) : 0;
