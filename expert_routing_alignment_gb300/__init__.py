@@ -133,6 +133,14 @@ EXPORTS = {
                                       ctypes.c_size_t, _P]),
     "moe_decode_block": (_I, [ctypes.POINTER(_LayerDesc), _P, _P, _P, ctypes.c_float, _I, _P, _P,
                               _P, _P, ctypes.c_size_t, _P, _P]),
+    "moe_quantize_nvfp4_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I]),
+    "moe_quantize_nvfp4": (_I, [_P, _L, _I, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _P,
+                                ctypes.c_size_t, _P]),
+    "moe_dequantize_nvfp4": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "moe_grouped_product_nvfp4": (_I, [ctypes.POINTER(_Proj), _I, _I, _I, _P, _P, _P, _I, _I, _I,
+                                       _P, _P, _I, _I, _P, _P, _P]),
+    "moe_grouped_gate_up_nvfp4": (_I, [ctypes.POINTER(_Proj), ctypes.POINTER(_Proj), _I, _I, _I,
+                                       _P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _P, _P, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -849,3 +857,211 @@ def moe_decode_block(layer: LayerDesc, x: torch.Tensor, residual: Optional[torch
         ctypes.pointer(layer._struct), x_at, r_at, w_at, eps, M, s_at, n_at, o_at,
         workspace.data_ptr(), workspace.numel(), e_at, _handle(stream, dev)))
     return sum_out, normed
+
+
+# --------------------------------------------------------------------------
+# four-bit rows, and the products of four-bit rows and weights
+# --------------------------------------------------------------------------
+
+_BYTES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _bytes_at(name: str, t: torch.Tensor, shape: tuple) -> int:
+    """The address of a dense buffer of bytes (scales: E4M3 values too)."""
+    if t.dtype not in _BYTES or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: want a contiguous uint8 tensor of shape {shape}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _packed(name: str, q) -> tuple:
+    """(codes, scale, global_scale) of a dict of moe_quantize_nvfp4, or of the
+    three tensors themselves."""
+    if isinstance(q, dict):
+        return q["codes"], q["scale"], q["global_scale"]
+    if len(q) != 3:
+        raise ValueError(f"{name}: want codes, scale and global_scale")
+    return tuple(q)
+
+
+def _packed_at(name: str, q, lead: tuple, cols: int) -> tuple:
+    """Their addresses, for codes of [*lead, cols / 2] bytes."""
+    codes, scale, glob = q
+    return (_bytes_at(f"{name} codes", codes, (*lead, cols // 2)),
+            _bytes_at(f"{name} scale", scale, (*lead, cols // 16)),
+            _at(f"{name} global_scale", glob, torch.float32, (lead[0],)))
+
+
+def quantize_nvfp4_workspace_bytes(groups: int, rows: int, cols: int) -> int:
+    nbytes = load().moe_quantize_nvfp4_workspace_bytes(groups, rows, cols)
+    if nbytes == 0:
+        raise MoeError("moe_quantize_nvfp4_workspace_bytes", MOE_EINVAL)
+    return nbytes
+
+
+def _quantized(name: str, x: torch.Tensor) -> tuple:
+    """(shape, type) of an output of moe_quantize_nvfp4 on x."""
+    *lead, cols = x.shape
+    if name == "codes":
+        return (*lead, cols // 2), torch.uint8
+    if name == "scale":
+        return (*lead, cols // 16), torch.uint8
+    if name == "global_scale":
+        return (lead[0],), torch.float32
+    if name == "values":
+        return tuple(x.shape), x.dtype
+    raise ValueError(f"no output {name!r}: want codes, scale, global_scale or values")
+
+
+def alloc_quantize_nvfp4_outputs(x: torch.Tensor,
+                                 want: Sequence[str] = ("codes", "scale", "global_scale"),
+                                 stream=None) -> dict:
+    """Buffers for moe_quantize_nvfp4 of x."""
+    return {name: _empty(*_quantized(name, x), x.device, stream) for name in want}
+
+
+def moe_quantize_nvfp4(x: torch.Tensor, want: Sequence[str] = ("codes", "scale", "global_scale"),
+                       global_scale: Optional[torch.Tensor] = None,
+                       tables: Optional[dict] = None, out: Optional[dict] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """x in NVFP4: rows [M, H], each with a global scale of its own, or expert
+    matrices [E, rows, cols], one for each expert; or under the scales that
+    ``global_scale`` gives.  "codes" uint8 [..., H / 2], "scale" uint8 (E4M3)
+    [..., H / 16], "global_scale" fp32 [M or E], and "values" of x's type and
+    shape, what the codes stand for (for products of the user's own and
+    gradients straight through the rounding).  With ``tables``, x's rows are in
+    expert order and the padding rows are skipped.  Writes the buffers of
+    ``out``, or new ones for the outputs in ``want``, and returns them by name."""
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x: want [M, H] or [E, rows, cols], got {tuple(x.shape)}")
+    dtype, kind, shape = x.dtype, _kind("x", x, _FLOAT), x.shape
+    groups, cols = shape[0], shape[-1]
+    rows = shape[1] if len(shape) == 3 else 1
+    if len(shape) == 3:
+        s0, s1, s2 = x.stride()
+        stride = s1 if rows > 1 else s0 if groups > 1 else cols
+        if (s2 != 1 and cols > 1) or (groups > 1 and rows > 1 and s0 != rows * s1):
+            raise ValueError(f"x: want evenly spaced dense rows, got strides {x.stride()}")
+    else:
+        stride = _row_stride("x", x, dtype, (groups, cols))
+    s_at, n = None, 0
+    if tables is not None:
+        sti = tables["sorted_token_ids"]
+        if len(shape) == 3 or _num_rows(tables) != groups:
+            raise ValueError(f"x: want the tables' {_num_rows(tables)} rows, got {tuple(shape)}")
+        s_at, n = _table("sorted_token_ids", sti, groups), tables["token_to_perm"].numel()
+    g_at = None
+    if global_scale is not None:
+        g_at = _at("global_scale", global_scale, torch.float32, (groups,))
+    at = {}
+    if out is not None:
+        for name, t in out.items():
+            oshape, otype = _quantized(name, x)
+            at[name] = _bytes_at(name, t, oshape) if otype is torch.uint8 else \
+                _at(name, t, otype, oshape)
+    dev = _on_device(x, global_scale, workspace, *(() if tables is None else (sti,)),
+                     *(() if out is None else out.values()))
+    if out is None:
+        out = {}
+        for name in want:
+            t = out[name] = _empty(*_quantized(name, x), x.device, stream)
+            at[name] = t.data_ptr()
+    nbytes, ws_at = 0, None
+    if rows > 1 and g_at is None:
+        if workspace is None:
+            workspace = _empty((quantize_nvfp4_workspace_bytes(groups, rows, cols),), torch.uint8,
+                               x.device, stream)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace: want a contiguous tensor")
+        ws_at, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    get = at.get
+    _check("moe_quantize_nvfp4", load().moe_quantize_nvfp4(
+        x.data_ptr(), stride, kind, groups, rows, cols, g_at, s_at, n, get("codes"), get("scale"),
+        get("global_scale"), get("values"), ws_at, nbytes, _handle(stream, dev)))
+    return out
+
+
+def moe_dequantize_nvfp4(codes: torch.Tensor, scale: torch.Tensor, global_scale: torch.Tensor,
+                         dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """The values of NVFP4 codes [M, H / 2] or [E, rows, cols / 2], of ``dtype``
+    (or out's type): code * (scale * global_scale), rounded once."""
+    if codes.dim() not in (2, 3):
+        raise ValueError(f"codes: want [M, H / 2] or [E, rows, cols / 2], got {tuple(codes.shape)}")
+    lead, cols = tuple(codes.shape[:-1]), 2 * codes.shape[-1]
+    c_at, s_at, g_at = _packed_at("rows", (codes, scale, global_scale), lead, cols)
+    if out is not None:
+        dtype = out.dtype
+    kind = _FLOAT.get(dtype)
+    if kind is None:
+        raise ValueError(f"out: unsupported type {dtype}")
+    o_at = None if out is None else _at("out", out, dtype, (*lead, cols))
+    dev = _on_device(codes, scale, global_scale, out)
+    if o_at is None:
+        out = _empty((*lead, cols), dtype, codes.device, stream)
+        o_at = out.data_ptr()
+    _check("moe_dequantize_nvfp4", load().moe_dequantize_nvfp4(
+        c_at, s_at, g_at, lead[0], lead[1] if len(lead) == 2 else 1, cols, kind, o_at,
+        _handle(stream, dev)))
+    return out
+
+
+def _grouped_nvfp4(fn: str, sets: tuple, rows, tables: dict, top_k: int, M: Optional[int],
+                   out: Optional[torch.Tensor], out_dtype: Optional[torch.dtype], err_word,
+                   stream) -> torch.Tensor:
+    sets = tuple(_packed("weight", w) for w in sets)
+    if sets[0][0].dim() != 3:
+        raise ValueError(f"weight codes: want [E, rows, cols / 2], got {tuple(sets[0][0].shape)}")
+    E, R, C = sets[0][0].shape
+    C *= 2
+    projs = []
+    for w in sets:
+        projs.append(_Proj(*_packed_at("weight", w, (E, R), C)))
+    codes, scale, glob = _packed("rows", rows)
+    by_token, n_rows = M is None, _num_rows(tables)
+    if by_token:
+        M = codes.shape[0]
+    x_at = _packed_at("rows", (codes, scale, glob), (M if by_token else n_rows,), C)
+    offs, sti = tables["expert_offsets"], tables["sorted_token_ids"]
+    f_at, s_at = _table("expert_offsets", offs, E + 1), _table("sorted_token_ids", sti, n_rows)
+    e_at = _err(err_word)
+    otype = out_dtype or (torch.bfloat16 if out is None else out.dtype)
+    okind = _FLOAT.get(otype)
+    if okind is None:
+        raise ValueError(f"out: unsupported type {otype}")
+    o_at = None if out is None else _at("out", out, otype, (n_rows, R))
+    dev = _on_device(codes, scale, glob, *(t for w in sets for t in w), offs, sti, out, err_word)
+    if o_at is None:
+        out = _empty((n_rows, R), otype, codes.device, stream)
+        o_at = out.data_ptr()
+    _check(fn, getattr(load(), fn)(
+        *(ctypes.byref(p) for p in projs), E, R, C, *x_at, int(by_token), M, top_k, f_at, s_at,
+        n_rows, okind, o_at, e_at, _handle(stream, dev)))
+    return out
+
+
+def moe_grouped_product_nvfp4(weight, rows, tables: dict, top_k: int, M: Optional[int] = None,
+                              out: Optional[torch.Tensor] = None,
+                              out_dtype: Optional[torch.dtype] = None,
+                              err_word: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """out [max_total, R] = each real position's row times its expert's matrix:
+    weight (codes [E, R, C / 2], scale, global_scale) and rows (the same of
+    moe_quantize_nvfp4, as its dict or in that order), four bits both.  Without
+    M the rows are the tokens' own, read through the tables; with M, the number
+    of tokens, they are in expert order, [max_total, C].  out has out_dtype
+    (bf16 by default); its padding rows stay as they were (undefined in a new
+    buffer)."""
+    return _grouped_nvfp4("moe_grouped_product_nvfp4", (weight,), rows, tables, top_k, M, out,
+                          out_dtype, err_word, stream)
+
+
+def moe_grouped_gate_up_nvfp4(gate, up, rows, tables: dict, top_k: int, M: Optional[int] = None,
+                              out: Optional[torch.Tensor] = None,
+                              out_dtype: Optional[torch.dtype] = None,
+                              err_word: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """moe_grouped_product_nvfp4 with two sets of the same sizes:
+    out = silu(rows x gate) * (rows x up), in fp32 before its rounding."""
+    return _grouped_nvfp4("moe_grouped_gate_up_nvfp4", (gate, up), rows, tables, top_k, M, out,
+                          out_dtype, err_word, stream)

@@ -13,25 +13,6 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr float kE4m3Max = 448.f;
 constexpr float kScaleMin = 1.17549435e-38f;   // 2^-126, the smallest normal
 
-// Maxima that keep a NaN: of two, and of three magnitudes.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// Two floats to E4M3, saturating, ties to even; the first in the low byte.
-__device__ __forceinline__ uint16_t to_e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // Sum over the threads of a row group (blockDim.x threads, whole warps):
 // butterfly in the warp, then the warps' sums four by four.  One barrier, of
 // the group alone; calls that follow one another take turns between two

@@ -604,6 +604,107 @@ int moe_decode_block(const moe_layer_desc *layer, const uint16_t *x,
                      uint16_t *out, void *workspace, size_t workspace_bytes,
                      uint32_t *err_word, void *stream);
 
+/* ---- four-bit rows and products ------------------------------------------ */
+
+/* Rows and expert weights in NVFP4, and the grouped products of both
+ * ("forward_nvfp4_grouped_decode.rs": the NVFP4 expert layer, whose grouped
+ * launchers take 16-bit rows; here the rows have four bits too, any number of
+ * them).  The pages print no quantisation; this is the format's own:
+ *   elements come in groups of rows x cols with a global scale each (rows = 1:
+ *   a scale for each token row; an expert's matrix otherwise) and in blocks of
+ *   16 neighbours in a row, in fp32 with every operation rounded:
+ *     g    = max(max|x| / 2688, 2^-80), the maximum over the blocks that have
+ *            neither NaN nor infinity; or as given
+ *     s    = e4m3(min(max|block| / (6 g), 448)); NaN for the other blocks
+ *     t    = s * g
+ *     code = e2m1(x / t), ties to even, at most 6; 0 where s is 0 or NaN
+ *   and an element's value is code * t.
+ * Layout, as moe_proj's NVFP4_G16: codes [groups][rows][cols/2] bytes, element
+ * 2i in the low nibble; scale [groups][rows][cols/16] E4M3 bytes; global_scale
+ * [groups] float. */
+
+/* Host only.  Workspace bytes moe_quantize_nvfp4 needs for groups of several
+ * rows without given scales (0: sizes it would refuse). */
+size_t moe_quantize_nvfp4_workspace_bytes(int groups, int rows, int cols);
+
+/* Quantisation of x [groups * rows][cols] of type dtype (BF16, F16, F32), rows
+ * x_stride apart.  given_scale [groups] or NULL: the global scales to use,
+ * each in [2^-80, 2^100].  codes, scale, global_scale and values, each of which
+ * may be NULL (not all): values [groups * rows][cols] of type dtype are what
+ * the codes stand for, rounded once (a value may round to infinity in F16).
+ *   sorted_token_ids [groups] or NULL (rows = 1 only): rows in expert order;
+ *   a row whose id is outside [0, num_slots) is left as it was.
+ *   workspace: needed for rows > 1 without given_scale, 16-byte aligned, at
+ *   least moe_quantize_nvfp4_workspace_bytes; needs no clearing, and calls
+ *   that overlap on the GPU need one each.
+ * groups = 0 is valid.  cols: a multiple of 16 up to MOE_MAX_ROW_HIDDEN; rows
+ * of whole 16-byte pieces, 16-byte aligned, are the fast ones.  Outputs overlap
+ * no input, but values may be x's own buffer when x is dense.
+ * Errors: MOE_EINVAL (NULL, sizes, strides, types, misaligned: codes 8 bytes,
+ * others their elements; a missing or short workspace; values on a strided
+ * x's buffer), MOE_EUNSUPPORTED
+ * (cols, groups * rows beyond int32, sorted_token_ids with rows > 1). */
+int moe_quantize_nvfp4(const void *x, int64_t x_stride, int dtype, int groups,
+                       int rows, int cols, const float *given_scale,
+                       const int32_t *sorted_token_ids, int num_slots,
+                       uint8_t *codes, uint8_t *scale, float *global_scale,
+                       void *values, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/* The values of codes: out[groups * rows][cols] of type dtype = code * (s * g),
+ * rounded once.  Sizes and errors as moe_quantize_nvfp4. */
+int moe_dequantize_nvfp4(const uint8_t *codes, const uint8_t *scale,
+                         const float *global_scale, int groups, int rows,
+                         int cols, int dtype, void *out, void *stream);
+
+/* Grouped product of four-bit rows and four-bit weights on the block-scaled
+ * tensor cores ("fp8_moe_grouped.rs", the grouped launchers' tensor-core
+ * twins; "forward_nvfp4_grouped_decode.rs").  For every real position p of
+ * expert e's run (expert_offsets[e] <= p < expert_offsets[e+1], slot i =
+ * sorted_token_ids[p] in [0, M * top_k)), with r = i / top_k if by_token, else
+ * r = p:
+ *   out[p][o] = T( sum_k code * s products, in fp32, times the global scale of
+ *                  row r, times that of expert e )
+ * weight: the matrices [num_experts][out_dim][in_dim] (one moe_proj in
+ * NVFP4_G16), codes, scale, global_scale: the rows, [M][in_dim] by token or
+ * [num_rows][in_dim] in expert order.  expert_offsets, sorted_token_ids and
+ * num_rows (the tables' max_total) as moe_align writes them for n = M * top_k.
+ *   out [num_rows][out_dim] of out_dtype (BF16, F16, F32): rows of real
+ *   positions are written, all others stay as they were.
+ * The product of a gradient with the experts' weights is the same call on a
+ * set of the transposed matrices, quantised along the other side.
+ * Any number of rows for each expert; M = 0 is valid.  in_dim: a multiple of 32
+ * up to MOE_MAX_ROW_HIDDEN (multiples of 256 are fast), any out_dim up to
+ * 4 * MOE_MAX_ROW_HIDDEN.  Deterministic, and a row's bits do not depend on the
+ * rows around it.  A NaN scale makes NaN of the rows (or features) it belongs
+ * to alone.
+ * Device errors: MOE_ERR_BAD_POSITION (offsets that do not ascend or leave the
+ * rows: nothing is computed; a slot outside [0, n]: skipped), MOE_ERR_TIMEOUT.
+ * Errors: MOE_EINVAL (NULL, sizes, types, misaligned: codes and scales 16
+ * bytes, others their elements), MOE_EUNSUPPORTED (in_dim, out_dim, top_k,
+ * num_experts, M * top_k, num_experts * out_dim beyond int32). */
+int moe_grouped_product_nvfp4(const moe_proj *weight, int num_experts, int out_dim,
+                              int in_dim, const uint8_t *codes,
+                              const uint8_t *scale, const float *global_scale,
+                              int by_token, int M, int top_k,
+                              const int32_t *expert_offsets,
+                              const int32_t *sorted_token_ids, int num_rows,
+                              int out_dtype, void *out, uint32_t *err_word,
+                              void *stream);
+
+/* The gate and up products of the same rows and their SiLU product
+ * (moe_grouped_gate_up on four-bit rows):
+ *   out[p][o] = T( silu(g) * u ), g and u as moe_grouped_product_nvfp4's sums in
+ * fp32 with gate's and up's matrices.  Everything else as there. */
+int moe_grouped_gate_up_nvfp4(const moe_proj *gate, const moe_proj *up,
+                              int num_experts, int out_dim, int in_dim,
+                              const uint8_t *codes, const uint8_t *scale,
+                              const float *global_scale, int by_token, int M,
+                              int top_k, const int32_t *expert_offsets,
+                              const int32_t *sorted_token_ids, int num_rows,
+                              int out_dtype, void *out, uint32_t *err_word,
+                              void *stream);
+
 #ifdef __cplusplus
 }
 #endif
