@@ -12,10 +12,13 @@
 // and of the row are factors of the whole sum.
 //
 // How, on sm_103a:
-//  * The weights are the MMA's M side, 128 output features a tile, two tiles
-//    (gate and up, or two neighbours of one matrix) over the same rows, which
-//    are its N side: a run of few rows costs few columns, and each weight tile
-//    is read once for up to 128 rows.
+//  * A tile is up to 128 rows by 256 weight rows: 128 features of gate and of
+//    up, or 256 neighbours of one matrix.  With many rows the tokens are the
+//    MMA's 128 lanes and the weights its 256 columns, so that a thread of the
+//    epilogue has neighbouring features of one row and stores whole sectors.
+//    With few the weights are the lanes and the tokens the columns (16 or 32):
+//    the epilogue is as short as the rows are few.  Both read the same shared
+//    memory and the same scales.
 //  * A stage is 256 k: 128 bytes a row, the width of the swizzle.  Weight
 //    tiles come by TMA boxes, rows by TMA gathers of four at a time, which
 //    take any rows: tokens need not be copied into expert order first.
@@ -27,9 +30,11 @@
 //  * A persistent CTA an SM walks over (expert, feature tile, row tile), the
 //    row tiles innermost: CTAs next to one another share weights, and an
 //    expert's rows stay in L2.
-//  * Roles: warp 0 copies, warp 1 issues MMAs, warps 4-7 bring the scales,
-//    warps 8-15 the epilogue.  Every wait gives up after about two seconds
-//    with MOE_ERR_TIMEOUT.
+//  * Roles: warp 0 copies, warp 1 issues MMAs, warp 2 looks the tiles up ahead
+//    of all others, warps 4-7 bring the scales, warps 8-15 the epilogue, which
+//    takes the accumulators into registers first, so that the next tile's MMAs
+//    run beside its arithmetic and stores.  The roles meet at mbarriers alone;
+//    every wait gives up after about two seconds with MOE_ERR_TIMEOUT.
 #include <cstring>
 
 #include "nvfp4.cuh"
@@ -46,17 +51,26 @@ constexpr int kTileRows = 128;             // rows of a row tile, features of a 
 constexpr int kOperand = 128 * 128;        // bytes of a stage's codes of 128 rows
 constexpr int kScales = 128 * 16;          // and of their scales
 constexpr int kStageBytes = 3 * kOperand;  // two weight tiles, the rows
-constexpr int kScaleWarp0 = 4, kEpi0 = 8;
-constexpr int kWarps = 16, kThreads = kWarps * 32;
-constexpr int kEpiThreads = (kWarps - kEpi0) * 32;
-// Tensor memory: two accumulators of 128 columns, then a ring of the stages'
-// scales, 16 columns for each operand (4 steps x 128 rows / 32).
-constexpr uint32_t kAccCols = 128, kScaleBase = 2 * kAccCols, kScaleCols = 48;
+constexpr int kScaleWarp0 = 4, kScaleWarps = 4, kEpi0 = 8, kEpiWarps = 8;
+constexpr int kWarps = kEpi0 + kEpiWarps, kThreads = kWarps * 32;
+// Registers a thread, of the kLaunchRegs that the block starts with: the
+// epilogue holds 128 accumulators.  Three shares of a warpgroup each (of four
+// warps), and no more in all than the block has.
+constexpr int kLaunchRegs = 128, kIssueRegs = 48, kScaleRegs = 96, kEpiRegs = 184;
+static_assert((kIssueRegs + kScaleRegs) * 128 + kEpiRegs * 256 <= kLaunchRegs * kThreads,
+              "registers");
+constexpr int kInfos = 4;                  // tiles looked up ahead
+constexpr int kFewRows = 32;               // rows that are columns
+// Tensor memory: the accumulators of 256 columns, then a ring of the stages'
+// scales: for each of 4 steps of 64 k, 8 columns of the weights' 256 rows; for
+// each, 4 columns of the tile's 128 rows.
+constexpr uint32_t kTileCols = 128, kScaleBase = 256, kScaleCols = 48, kRowScales = 32;
 
 struct ProductArgs {
   int E, R, K;               // experts, output features, input features
   int by_token, top_k, n;    // n slots
   int num_rows;              // of the expert-order buffers
+  int align;                 // of the output's rows, in bytes: 32, 16 or less
   int feature_tiles;         // pairs of tiles (or gate and up tiles) of an expert
   const int32_t *offsets, *sti;
   const uint8_t *wscale[2];  // [E][R][K / 16] of the two tiles' matrices
@@ -72,12 +86,20 @@ struct ProductMaps {
   CUtensorMap w[2], x;
 };
 
+// A tile as every role reads it; rows < 0: no more tiles.
+struct TileInfo {
+  int e, m, p0, rows;       // expert, feature tile, first position, rows up to the last real one
+  int row[kTileRows];       // the row that each position reads, -1: none
+  float xg[kTileRows];      // its global scale
+};
+
 struct Smem {
   alignas(1024) uint8_t codes[kStages][kStageBytes];
   alignas(16) uint8_t scales[kStages][3 * kScales];
-  float xg[kTileRows];         // the rows' global scales
-  int valid[kTileRows];
-  uint64_t full[kStages], empty[kStages], acc_full, acc_empty, drain;
+  alignas(16) TileInfo info[kInfos];
+  uint64_t full[kStages], empty[kStages], copied[kStages];
+  uint64_t info_full[kInfos], info_empty[kInfos];
+  uint64_t acc_full, acc_empty, drain;
   int failed;
   uint32_t tmem;
   int warp_sum[kWarps];
@@ -101,14 +123,43 @@ __device__ __forceinline__ void mma_nvf4(uint32_t d, uint64_t ad, uint64_t bd, u
       " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
       "l"(ad), "l"(bd), "r"(id), "r"(sa), "r"(sb), "r"(acc));
 }
-// 16 consecutive 32-bit columns of this warp's 32 TMEM lanes, from registers.
+// 32 consecutive fp32 columns of this warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31"
+      "}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr));
+}
+// 16 or 32 consecutive 32-bit columns of this warp's 32 TMEM lanes, from registers.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15])
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16"
+      "};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+      "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
+      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32"
+      "};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+      "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 // Rows r0..r3 (from column x) of a two-dimensional map, 128 bytes each, to dst.
@@ -134,54 +185,7 @@ __device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x,
 // tiles
 // ---------------------------------------------------------------------------
 
-struct Tile {
-  int e, m, p0, len;   // expert, feature tile, first position, positions to the run's end (<= 128)
-};
-
 __device__ __forceinline__ int clamp_to(int v, int hi) { return v < 0 ? 0 : v > hi ? hi : v; }
-
-__device__ __forceinline__ Tile tile_of(const ProductArgs &a, const Smem &S, int idx) {
-  const int mt = a.feature_tiles;
-  int lo = 0, hi = a.E - 1;   // the last expert whose tiles begin at or ahead of idx
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (S.tiles[mid] * mt <= idx)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  const int rt = S.tiles[lo + 1] - S.tiles[lo], r = idx - S.tiles[lo] * mt;
-  const int begin = clamp_to(a.offsets[lo], a.num_rows);
-  const int end = clamp_to(a.offsets[lo + 1], a.num_rows);
-  Tile t;
-  t.e = lo;
-  t.m = r / rt;
-  t.p0 = begin + (r - t.m * rt) * kTileRows;
-  t.len = min(kTileRows, end - t.p0);
-  return t;
-}
-
-// The row that position p0 + i of a tile reads, or -1 where there is none.
-__device__ __forceinline__ int row_at(const ProductArgs &a, const Tile &t, int i) {
-  if (i >= t.len) return -1;
-  const int s = a.sti[t.p0 + i];
-  if ((unsigned)s >= (unsigned)a.n) return -1;
-  return a.by_token ? s / a.top_k : t.p0 + i;
-}
-// Rows i = 4 * lane + 0..3 of a tile; returns the tile's rows (the last real
-// one's place + 1), the same in every lane.
-__device__ __forceinline__ int tile_rows(const ProductArgs &a, const Tile &t, int lane,
-                                         int (&r)[4]) {
-  int last = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    r[j] = row_at(a, t, 4 * lane + j);
-    if (r[j] >= 0) last = 4 * lane + j + 1;
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) last = max(last, __shfl_xor_sync(kFull, last, d));
-  return last;
-}
 
 __device__ __forceinline__ void fail(Smem &S, const ProductArgs &a) {
   *(volatile int *)&S.failed = 1;
@@ -191,55 +195,128 @@ __device__ __forceinline__ bool wait_all(Smem &S, uint64_t *bar, uint32_t parity
   return __all_sync(kFull, wait_phase(&S.failed, bar, parity));
 }
 
+// Warp 2: the CTA's tiles in order, without those of padding alone.
+__device__ void scheduler(const ProductArgs &a, Smem &S, int total) {
+  const int lane = threadIdx.x & 31, mt = a.feature_tiles;
+  uint32_t n = 0;
+  for (int idx = blockIdx.x;; idx += gridDim.x) {
+    int e = 0, m = 0, p0 = 0, rows = -1, r[4];
+    float xg[4];
+    if (idx < total) {
+      int hi = a.E - 1;   // e: the last expert whose tiles begin at or ahead of idx
+      while (e < hi) {
+        const int mid = (e + hi + 1) >> 1;
+        if (S.tiles[mid] * mt <= idx)
+          e = mid;
+        else
+          hi = mid - 1;
+      }
+      const int rt = S.tiles[e + 1] - S.tiles[e], at = idx - S.tiles[e] * mt;
+      m = at / rt;
+      p0 = clamp_to(a.offsets[e], a.num_rows) + (at - m * rt) * kTileRows;
+      const int len = min(kTileRows, clamp_to(a.offsets[e + 1], a.num_rows) - p0);
+      rows = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = 4 * lane + j;
+        const int s = i < len ? a.sti[p0 + i] : a.n;
+        r[j] = (unsigned)s >= (unsigned)a.n ? -1 : a.by_token ? s / a.top_k : p0 + i;
+        if (r[j] >= 0) rows = i + 1;
+        if ((s < 0 || s > a.n) && a.err) atomicOr(a.err, MOE_ERR_BAD_POSITION);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xg[j] = r[j] >= 0 ? a.xglobal[r[j]] : 0.f;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) rows = max(rows, __shfl_xor_sync(kFull, rows, d));
+      if (!rows) continue;
+    }
+    const int slot = n % kInfos;
+    if (n >= kInfos && !wait_all(S, &S.info_empty[slot], (n / kInfos - 1) & 1)) {
+      if (lane == 0) fail(S, a);
+      return;
+    }
+    TileInfo &t = S.info[slot];
+    if (lane == 0) *reinterpret_cast<int4 *>(&t.e) = make_int4(e, m, p0, rows);
+    if (rows > 0) {
+      *reinterpret_cast<int4 *>(&t.row[4 * lane]) = make_int4(r[0], r[1], r[2], r[3]);
+      *reinterpret_cast<float4 *>(&t.xg[4 * lane]) = make_float4(xg[0], xg[1], xg[2], xg[3]);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.info_full[slot]);
+    if (rows < 0) return;
+    ++n;
+  }
+}
+
+// A role's view of the tiles: next() gives the next one (NULL at the end, or
+// after a failure, which sets ok = false), done() lets go of it.  Whole warps.
+struct Tiles {
+  Smem &S;
+  uint32_t n = 0;
+  bool ok = true;
+  __device__ __forceinline__ explicit Tiles(Smem &s) : S(s) {}
+  __device__ __forceinline__ const TileInfo *next() {
+    const TileInfo *t = &S.info[n % kInfos];
+    if (!wait_all(S, &S.info_full[n % kInfos], (n / kInfos) & 1)) {
+      ok = false;
+      return nullptr;
+    }
+    return t->rows < 0 ? nullptr : t;
+  }
+  __device__ __forceinline__ void done() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&S.info_empty[n % kInfos]);
+    ++n;
+  }
+};
+
 // ---------------------------------------------------------------------------
 // roles
 // ---------------------------------------------------------------------------
 
+// Whether a tile has its second 128 features, and the first feature of half j.
 template <bool kPair>
-__device__ __forceinline__ bool second_tile(const ProductArgs &a, const Tile &t) {
-  return kPair || t.m * 256 + 128 < a.R;
+__device__ __forceinline__ bool second_half(const ProductArgs &a, int m) {
+  return kPair || m * 256 + 128 < a.R;
 }
-// The first feature of tile j of a pair.
 template <bool kPair>
-__device__ __forceinline__ int feature_of(const Tile &t, int j) {
-  return kPair ? t.m * 128 : t.m * 256 + j * 128;
+__device__ __forceinline__ int feature_of(int m, int j) {
+  return kPair ? m * 128 : m * 256 + j * 128;
 }
 
 template <bool kPair>
-__device__ void producer(const ProductArgs &a, const ProductMaps &maps, Smem &S, int total) {
+__device__ void producer(const ProductArgs &a, const ProductMaps &maps, Smem &S) {
   const int lane = threadIdx.x & 31, kbs = (a.K + 255) / 256;
   uint32_t s = 0;
-  bool ok = true;
-  for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-    const Tile t = tile_of(a, S, idx);
-    int r[4];
-    const int rows = tile_rows(a, t, lane, r);
-    if (!rows) continue;
-    const bool two = second_tile<kPair>(a, t);
+  Tiles tiles(S);
+  while (const TileInfo *t = tiles.next()) {
+    const int rows = t->rows, m = t->m, w0 = t->e * a.R;
+    const int4 r4 = *reinterpret_cast<const int4 *>(&t->row[4 * lane]);
+    tiles.done();
+    const bool two = second_half<kPair>(a, m);
     const uint32_t bytes = (two ? 2 : 1) * kOperand + (rows + 3) / 4 * 512;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = max(r[j], 0);
     for (int kb = 0; kb < kbs; ++kb, ++s) {
       const int slot = s % kStages;
       uint64_t *bar = &S.full[slot];
       if (s >= kStages && !wait_all(S, &S.empty[slot], (s / kStages - 1) & 1)) {
-        ok = false;
+        tiles.ok = false;
         break;
       }
       uint8_t *dst = S.codes[slot];
       if (lane == 0) {
         mbar_expect_tx(bar, bytes);
-        tma_2d(dst, &maps.w[0], kb * 128, t.e * a.R + feature_of<kPair>(t, 0), bar);
+        tma_2d(dst, &maps.w[0], kb * 128, w0 + feature_of<kPair>(m, 0), bar);
         if (two)
-          tma_2d(dst + kOperand, &maps.w[1], kb * 128, t.e * a.R + feature_of<kPair>(t, 1), bar);
+          tma_2d(dst + kOperand, &maps.w[1], kb * 128, w0 + feature_of<kPair>(m, 1), bar);
       }
       __syncwarp();
       if (4 * lane < rows)
-        tma_gather4(dst + 2 * kOperand + lane * 512, &maps.x, kb * 128, r[0], r[1], r[2], r[3],
-                    bar);
+        tma_gather4(dst + 2 * kOperand + lane * 512, &maps.x, kb * 128, max(r4.x, 0),
+                    max(r4.y, 0), max(r4.z, 0), max(r4.w, 0), bar);
     }
+    if (!tiles.ok) break;
   }
-  if (!ok && lane == 0) fail(S, a);
+  if (!tiles.ok && lane == 0) fail(S, a);
   // no copy may be in flight when the CTA ends
   for (uint32_t j = s < kStages ? 0 : s - kStages; j < s; ++j) {
     const uint64_t t0 = gtime();
@@ -249,48 +326,51 @@ __device__ void producer(const ProductArgs &a, const ProductMaps &maps, Smem &S,
 }
 
 template <bool kPair>
-__device__ void mma_issuer(const ProductArgs &a, Smem &S, int total, uint32_t tmem) {
+__device__ void mma_issuer(const ProductArgs &a, Smem &S, uint32_t tmem) {
   const int lane = threadIdx.x & 31, kbs = (a.K + 255) / 256;
-  uint32_t s = 0, n = 0;
-  bool ok = true;
-  for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-    const Tile t = tile_of(a, S, idx);
-    int r[4];
-    const int rows = tile_rows(a, t, lane, r);
-    if (!rows) continue;
-    const bool two = second_tile<kPair>(a, t);
-    const uint32_t id = idesc_nvf4((rows + 15) / 16 * 16);
-    if (n && !wait_all(S, &S.acc_empty, (n - 1) & 1)) {
-      ok = false;
+  uint32_t s = 0;
+  Tiles tiles(S);
+  while (const TileInfo *t = tiles.next()) {
+    const int rows = t->rows;
+    const bool two = second_half<kPair>(a, t->m), few = rows <= kFewRows;
+    tiles.done();
+    const uint32_t id = idesc_nvf4(few ? (rows + 15) / 16 * 16 : two ? 256 : 128);
+    if (tiles.n > 1 && !wait_all(S, &S.acc_empty, tiles.n & 1)) {
+      tiles.ok = false;
       break;
     }
     tc_fence_after();
     for (int kb = 0; kb < kbs; ++kb, ++s) {
       const int slot = s % kStages;
       if (!wait_all(S, &S.full[slot], (s / kStages) & 1)) {
-        ok = false;
+        tiles.ok = false;
         break;
       }
       tc_fence_after();
       if (lane == 0) {
-        const int steps = min(4, (a.K - kb * 256 + 63) / 64);
+        const int steps = min(4, (a.K - kb * 256 + 63) / 64);   // 64 k: 32 bytes of the row
         const uint32_t codes = smem_addr(S.codes[slot]);
-        const uint64_t bd = sdesc(codes + 2 * kOperand);
+        const uint64_t w = sdesc(codes), x = sdesc(codes + 2 * kOperand);
         const uint32_t sc = tmem + kScaleBase + slot * kScaleCols;
-        for (int j = 0; j < (two ? 2 : 1); ++j) {
-          const uint64_t ad = sdesc(codes + j * kOperand);
-          for (int i = 0; i < steps; ++i)   // 64 k: 32 bytes on in the swizzled row
-            mma_nvf4(tmem + j * kAccCols, ad + 2 * i, bd + 2 * i, id, sc + j * 16 + 4 * i,
-                     sc + 32 + 4 * i, (kb | i) != 0);
+        for (int i = 0; i < steps; ++i) {
+          const uint32_t acc = (kb | i) != 0, sx = sc + kRowScales + 4 * i;
+          if (few) {
+            mma_nvf4(tmem, w + 2 * i, x + 2 * i, id, sc + 8 * i, sx, acc);
+            if (two)
+              mma_nvf4(tmem + kTileCols, w + (kOperand >> 4) + 2 * i, x + 2 * i, id,
+                       sc + 8 * i + 4, sx, acc);
+          } else {
+            mma_nvf4(tmem, x + 2 * i, w + 2 * i, id, sx, sc + 8 * i, acc);
+          }
         }
         mma_commit(&S.empty[slot]);
         if (kb == kbs - 1) mma_commit(&S.acc_full);
       }
       __syncwarp();
     }
-    ++n;
+    if (!tiles.ok) break;
   }
-  if (!ok && lane == 0) fail(S, a);
+  if (!tiles.ok && lane == 0) fail(S, a);
   // tensor memory is given back only after the last MMA
   if (lane == 0) {
     mma_commit(&S.drain);
@@ -333,35 +413,32 @@ template <bool kPair, int ALIGN>
 struct ScaleWalk {
   const ProductArgs &a;
   Smem &S;
-  int total, idx, kb, kbs, thread;
-  uint32_t issued;
+  Tiles tiles;
+  int kb, kbs, thread;
+  bool end = false;
+  uint32_t issued = 0;
   const uint8_t *row[3];   // this thread's rows of the tile's operands, NULL: none
 
-  __device__ ScaleWalk(const ProductArgs &args, Smem &sm, int tot)
-      : a(args), S(sm), total(tot), idx((int)blockIdx.x - (int)gridDim.x), kb(0),
-        kbs((args.K + 255) / 256), thread((int)threadIdx.x - kScaleWarp0 * 32), issued(0) {
-    kb = kbs;
-  }
+  __device__ __forceinline__ ScaleWalk(const ProductArgs &args, Smem &sm)
+      : a(args), S(sm), tiles(sm), kb((args.K + 255) / 256), kbs(kb),
+        thread((int)threadIdx.x - kScaleWarp0 * 32) {}
   // The next stage's copies (one group, empty behind the end).
   __device__ __forceinline__ void next() {
-    while (kb == kbs) {
-      idx += gridDim.x;
-      if (idx >= total) {
-        idx = total;
-        break;
-      }
-      const Tile t = tile_of(a, S, idx);
-      int r[4];
-      if (!tile_rows(a, t, thread & 31, r)) continue;
-      const int pitch = a.K / 16;
+    if (kb == kbs && !end) {
+      if (const TileInfo *t = tiles.next()) {
+        const int pitch = a.K / 16;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int f = feature_of<kPair>(t, j) + thread;
-        row[j] = f < a.R ? a.wscale[j] + ((int64_t)t.e * a.R + f) * pitch : nullptr;
+        for (int j = 0; j < 2; ++j) {
+          const int f = feature_of<kPair>(t->m, j) + thread;
+          row[j] = f < a.R ? a.wscale[j] + ((int64_t)t->e * a.R + f) * pitch : nullptr;
+        }
+        const int x = t->row[thread];
+        row[2] = x >= 0 ? a.xscale + (int64_t)x * pitch : nullptr;
+        tiles.done();
+        kb = 0;
+      } else {
+        end = true;
       }
-      const int x = row_at(a, t, thread);
-      row[2] = x >= 0 ? a.xscale + (int64_t)x * pitch : nullptr;
-      kb = 0;
     }
     if (kb < kbs) {
       uint8_t *dst = S.scales[issued % kStages] + thread * 16;
@@ -377,45 +454,57 @@ struct ScaleWalk {
 };
 
 // Warps 4-7.  Shared memory is a ring that these warps alone use: a slot is
-// written again by the copies of stage s + 3, which are started after the
-// barrier of stage s, when all have read stage s - 1.
+// written again by the copies of stage s + 3, which are started once all four
+// have met at stage s, each after it has read stage s - 1.
 template <bool kPair, int ALIGN>
-__device__ void scale_role(const ProductArgs &a, Smem &S, int total, uint32_t tmem) {
+__device__ void scale_role(const ProductArgs &a, Smem &S, uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kScaleBase;
-  ScaleWalk<kPair, ALIGN> walk(a, S, total);
+  ScaleWalk<kPair, ALIGN> walk(a, S);
   for (int d = 0; d < kStages - 1; ++d) walk.next();
   bool ok = true;
   for (uint32_t s = 0; s < walk.issued; ++s) {
     const int slot = s % kStages;
     copies_wait(kStages - 1);
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    uint32_t v[3][16];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.copied[slot]);
+    ok = wait_all(S, &S.copied[slot], (s / kStages) & 1);
+    if (!ok) break;
+    uint32_t w[32], x[16];   // column 8 i + 4 half + row / 32 of step i, and 4 i + row / 32
+    const uint8_t *from = S.scales[slot] + lane * 16;
 #pragma unroll
-    for (int j = 0; j < 3; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(S.scales[slot] + j * kScales +
-                                                         (q * 32 + lane) * 16);
-        v[j][q] = w.x;
-        v[j][4 + q] = w.y;
-        v[j][8 + q] = w.z;
-        v[j][12 + q] = w.w;
-      }
-    walk.next();
-    // after a failure the walk goes on, so that the four warps' barriers match
-    if (ok && s >= kStages && !wait_all(S, &S.empty[slot], (s / kStages - 1) & 1)) ok = false;
-    if (ok) {
-      tc_fence_after();
-#pragma unroll
-      for (int j = 0; j < 3; ++j) tmem_st16(base + slot * kScaleCols + j * 16, v[j]);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.full[slot]);
+    for (int q = 0; q < 8; ++q) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(from + q * 512);
+      w[q] = v.x;
+      w[8 + q] = v.y;
+      w[16 + q] = v.z;
+      w[24 + q] = v.w;
     }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(from + 2 * kScales + q * 512);
+      x[q] = v.x;
+      x[4 + q] = v.y;
+      x[8 + q] = v.z;
+      x[12 + q] = v.w;
+    }
+    walk.next();
+    if (s >= kStages) ok = wait_all(S, &S.empty[slot], (s / kStages - 1) & 1);
+    if (!ok) break;
+    tc_fence_after();
+    tmem_st32(base + slot * kScaleCols, w);
+    tmem_st16(base + slot * kScaleCols + kRowScales, x);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.full[slot]);
   }
-  if (!ok && lane == 0) fail(S, a);
+  if ((!ok || !walk.tiles.ok) && lane == 0) fail(S, a);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+__device__ __forceinline__ float silu_times(float g, float u) {
+  return __fdividef(g, 1.f + expf(-g)) * u;   // at most 2^126: 0 beyond, where it is below 2^-119
 }
 
 template <typename T>
@@ -427,64 +516,125 @@ __device__ __forceinline__ void store_one(void *out, int64_t at, float v) {
     static_cast<float *>(out)[at] = v;
 }
 
-__device__ __forceinline__ void epi_sync() {
-  asm volatile("bar.sync 2, %0;" ::"n"(kEpiThreads) : "memory");
+__device__ __forceinline__ void st_global_32(void *p, const uint32_t *w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// N neighbouring features of a row, in floats, from feature f on: whole sectors
+// of 32 bytes or pieces of 16 where rows allow them (`align`).
+template <typename T, int N>
+__device__ __forceinline__ void store_features(const ProductArgs &a, int64_t p, int f,
+                                               const uint32_t (&v)[N]) {
+  using TB = typename T::bits;
+  constexpr int PER = 32 / (int)sizeof(TB);   // elements of a sector
+  TB *dst = static_cast<TB *>(a.out) + p * a.R + f;
+  if (a.align >= 16) {
+#pragma unroll
+    for (int i = 0; i < N; i += PER) {
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (sizeof(TB) == 2)
+          w[j] = T::down2(__uint_as_float(v[i + 2 * j]), __uint_as_float(v[i + 2 * j + 1]));
+        else
+          w[j] = v[i + j];
+      }
+      if (a.align == 32) {
+        if (f + i < a.R) st_global_32(dst + i, w);
+      } else {
+        if (f + i < a.R) *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (f + i + PER / 2 < a.R)
+          *reinterpret_cast<uint4 *>(dst + i + PER / 2) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (f + i < a.R) store_one<T>(a.out, p * a.R + f + i, __uint_as_float(v[i]));
+  }
 }
 
 template <typename T, bool kPair>
-__device__ void epilogue(const ProductArgs &a, Smem &S, int total, uint32_t tmem) {
+__device__ void epilogue(const ProductArgs &a, Smem &S, uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3;
-  const int half = (warp - kEpi0) >> 2, thread = (int)threadIdx.x - kEpi0 * 32;
+  const int group = (warp - kEpi0) >> 2;
   const uint32_t base = tmem + ((uint32_t)(q * 32) << 16);
-  uint32_t n = 0;
-  bool ok = true;
-  for (int idx = blockIdx.x; idx < total; idx += gridDim.x) {
-    const Tile t = tile_of(a, S, idx);
-    int r[4];
-    const int rows = tile_rows(a, t, lane, r);
-    if (!rows) continue;
-    epi_sync();   // the tile before has been read
-    if (thread < kTileRows) {
-      const int x = row_at(a, t, thread);
-      S.valid[thread] = x >= 0;
-      S.xg[thread] = x >= 0 ? a.xglobal[x] : 0.f;
-      if (thread < t.len) {
-        const int slot = a.sti[t.p0 + thread];
-        if ((slot < 0 || slot > a.n) && a.err) atomicOr(a.err, MOE_ERR_BAD_POSITION);
-      }
+  Tiles tiles(S);
+  while (const TileInfo *t = tiles.next()) {
+    const int rows = t->rows, m = t->m, p0 = t->p0;
+    const bool few = rows <= kFewRows;
+    const float g0 = a.wglobal[0][t->e], g1 = a.wglobal[1][t->e];
+    if (!wait_all(S, &S.acc_full, tiles.n & 1)) {
+      tiles.ok = false;
+      break;
     }
-    epi_sync();
-    if (ok && !wait_all(S, &S.acc_full, n & 1)) ok = false;
-    ++n;
-    if (!ok) continue;   // the others' barriers match
     tc_fence_after();
-    const float g0 = a.wglobal[0][t.e], g1 = a.wglobal[1][t.e];
-    const int f0 = feature_of<kPair>(t, 0) + q * 32 + lane;
-    const int f1 = feature_of<kPair>(t, 1) + q * 32 + lane;
-    for (int c0 = half * 64; c0 < min(rows, half * 64 + 64); c0 += 16) {
+    if (few) {
+      // lanes are features, columns rows: 16 of them for each group
+      const int c0 = group * 16;
       uint32_t v0[16], v1[16];
-      tmem_ld16(base + c0, v0);
-      tmem_ld16(base + kAccCols + c0, v1);
-      tmem_wait_ld();
+      if (c0 < rows) {
+        tmem_ld16(base + c0, v0);
+        tmem_ld16(base + kTileCols + c0, v1);
+        tmem_wait_ld();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.acc_empty);
+      const int f0 = feature_of<kPair>(m, 0) + q * 32 + lane;
+      const int f1 = feature_of<kPair>(m, 1) + q * 32 + lane;
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        if (!S.valid[c0 + c]) continue;
-        const float xg = S.xg[c0 + c];
-        const int64_t at = (int64_t)(t.p0 + c0 + c) * a.R;
+        if (c0 + c >= rows || t->row[c0 + c] < 0) continue;
+        const float xg = t->xg[c0 + c];
+        const int64_t at = (int64_t)(p0 + c0 + c) * a.R;
         const float y0 = __uint_as_float(v0[c]) * xg * g0, y1 = __uint_as_float(v1[c]) * xg * g1;
         if constexpr (kPair) {
-          if (f0 < a.R) store_one<T>(a.out, at + f0, silu_f32(y0) * y1);
+          if (f0 < a.R) store_one<T>(a.out, at + f0, silu_times(y0, y1));
         } else {
           if (f0 < a.R) store_one<T>(a.out, at + f0, y0);
           if (f1 < a.R) store_one<T>(a.out, at + f1, y1);
         }
       }
+      tiles.done();
+      continue;
+    }
+    // lanes are rows, columns features: 128 for each group (64 of gate and of up)
+    const int i = q * 32 + lane;
+    const bool real = t->row[i] >= 0;
+    const float xg = t->xg[i];
+    tiles.done();
+    uint32_t v[4][32];
+    if (q * 32 < rows) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        tmem_ld32(base + (kPair ? (h >> 1) * kTileCols + group * 64 + (h & 1) * 32
+                                : group * kTileCols + h * 32),
+                  v[h]);
+      tmem_wait_ld();
     }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.acc_empty);
+    if (!real) continue;
+#pragma unroll
+    for (int h = 0; h < (kPair ? 2 : 4); ++h) {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const float y = __uint_as_float(v[h][c]) * xg * g0;
+        if constexpr (kPair)
+          v[h][c] = __float_as_uint(
+              silu_times(y, __uint_as_float(v[2 + h][c]) * xg * g1));
+        else
+          v[h][c] = __float_as_uint(y);
+      }
+      store_features<T>(a, p0 + i, (kPair ? m * 128 + group * 64 : m * 256 + group * 128) + h * 32,
+                        v[h]);
+    }
   }
-  if (!ok && lane == 0) fail(S, a);
+  if (!tiles.ok && lane == 0) fail(S, a);
 }
 
 template <typename T, bool kPair, int ALIGN>
@@ -496,11 +646,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&S.full[i], 5);    // the copies, and each scale warp
+      mbar_init(&S.full[i], 1 + kScaleWarps);   // the copies, and each scale warp
       mbar_init(&S.empty[i], 1);
+      mbar_init(&S.copied[i], kScaleWarps);
+    }
+    for (int i = 0; i < kInfos; ++i) {
+      mbar_init(&S.info_full[i], 1);
+      mbar_init(&S.info_empty[i], 2 + kScaleWarps + kEpiWarps);
     }
     mbar_init(&S.acc_full, 1);
-    mbar_init(&S.acc_empty, kWarps - kEpi0);
+    mbar_init(&S.acc_empty, kEpiWarps);
     mbar_init(&S.drain, 1);
     S.failed = 0;
     fence_mbar_init();
@@ -520,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();
 
-  // S.tiles: the row tiles ahead of each expert's, two experts a thread
+  // S.tiles: the row tiles ahead of each expert's, a thread's two experts at a time
   int run[2], bad = 0;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -553,14 +708,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const int total = refused ? 0 : S.tiles[a.E] * a.feature_tiles;
 
-  if (warp == 0)
-    producer<kPair>(a, maps, S, total);
-  else if (warp == 1)
-    mma_issuer<kPair>(a, S, total, tmem);
-  else if (warp >= kEpi0)
-    epilogue<T, kPair>(a, S, total, tmem);
-  else if (warp >= kScaleWarp0)
-    scale_role<kPair, ALIGN>(a, S, total, tmem);
+  if (warp >= kEpi0) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    epilogue<T, kPair>(a, S, tmem);
+  } else if (warp >= kScaleWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kScaleRegs));
+    scale_role<kPair, ALIGN>(a, S, tmem);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == 0)
+      producer<kPair>(a, maps, S);
+    else if (warp == 1)
+      mma_issuer<kPair>(a, S, tmem);
+    else if (warp == 2)
+      scheduler(a, S, total);
+  }
 
   tc_fence_before();
   __syncthreads();
@@ -575,8 +737,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 // host
 // ---------------------------------------------------------------------------
 
-constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;   // with its alignment
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
+
+// A warpgroup that asks for registers waits until the others have given up
+// theirs: a kernel that was built with fewer at launch must not run.
+int ensure_registers(const void *kernel) {
+  cudaFuncAttributes attr;
+  const cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
+  if (e != cudaSuccess) {
+    set_last_cuda_error(e);
+    return MOE_ECUDA;
+  }
+  return attr.numRegs == kLaunchRegs ? MOE_OK : MOE_EUNSUPPORTED;
+}
 
 bool misaligned(const void *p, uintptr_t bytes) { return ((uintptr_t)p & (bytes - 1)) != 0; }
 
@@ -622,6 +796,8 @@ int grouped(const moe_proj *w0, const moe_proj *w1, int E, int R, int K, const u
   a.xscale = scale;
   a.xglobal = global;
   a.out = out;
+  const uint64_t v = (uint64_t)(uintptr_t)out | (uint64_t)R * eb | 32;
+  a.align = (int)(v & (~v + 1));
   a.err = err;
   ProductMaps maps;
   memset(&maps, 0, sizeof(maps));
@@ -642,6 +818,7 @@ int grouped(const moe_proj *w0, const moe_proj *w1, int E, int R, int K, const u
     constexpr bool P = decltype(pair)::value;
     auto launch = [&](auto kernel) {
       if (const int st = ensure_smem_limit((const void *)kernel, kSmemBytes)) return st;
+      if (const int st = ensure_registers((const void *)kernel)) return st;
       return launch_pdl(kernel, grid, dim3(kThreads), kSmemBytes, stream, a, maps);
     };
     if (K % 256 == 0) return launch(grouped_nvfp4_kernel<T, P, 16>);
