@@ -20,18 +20,20 @@
 //    the epilogue is as short as the rows are few.  Both read the same shared
 //    memory and the same scales.
 //  * A stage is 256 k: 128 bytes a row, the width of the swizzle.  Weight
-//    tiles come by TMA boxes, rows by TMA gathers of four at a time, which
-//    take any rows: tokens need not be copied into expert order first.
-//  * Scales stay row-major as the format has them.  Four warps copy a stage's
-//    16 bytes a row to shared memory ahead (cp.async) and write them to tensor
-//    memory as the MMA reads them: lane = row % 32, column = row / 32, a
-//    column's four bytes the four blocks of one 64-k step, the same in all
-//    four quarters of the lanes.
+//    tiles come by TMA boxes, and so do rows in expert order; the tokens' own
+//    rows, which can be any, by 16-byte copies (cp.async) that
+//    place them as the swizzle would, so that tokens need not be copied into
+//    expert order first.  (TMA gathers of four rows each took the gate and up
+//    of 4096 rows from 91 to 150 us.)
+//  * Scales stay row-major as the format has them.  They are copied by
+//    words (4 blocks, 64 k) to where the tensor cores' own copy to tensor
+//    memory takes them (tcgen05.cp 32x128b, issued ahead of the stage's MMAs):
+//    for each 64 k and 128 rows 32 x 16 bytes, line = row % 32, word = row / 32.
 //  * A persistent CTA an SM walks over (expert, feature tile, row tile), the
 //    row tiles innermost: CTAs next to one another share weights, and an
 //    expert's rows stay in L2.
 //  * Roles: warp 0 copies, warp 1 issues MMAs, warp 2 looks the tiles up ahead
-//    of all others, warps 4-7 bring the scales, warps 8-15 the epilogue, which
+//    of all others, warps 4-7 bring the scales and tokens' rows, warps 8-15 the epilogue, which
 //    takes the accumulators into registers first, so that the next tile's MMAs
 //    run beside its arithmetic and stores.  The roles meet at mbarriers alone;
 //    every wait gives up after about two seconds with MOE_ERR_TIMEOUT.
@@ -49,15 +51,18 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kStages = 4;
 constexpr int kTileRows = 128;             // rows of a row tile, features of a feature tile
 constexpr int kOperand = 128 * 128;        // bytes of a stage's codes of 128 rows
-constexpr int kScales = 128 * 16;          // and of their scales
 constexpr int kStageBytes = 3 * kOperand;  // two weight tiles, the rows
-constexpr int kScaleWarp0 = 4, kScaleWarps = 4, kEpi0 = 8, kEpiWarps = 8;
+// The scales of a stage in shared memory: 512 bytes for each 64 k and 128 rows,
+// set apart so that a warp's words of 8 rows x 4 steps lie in 32 banks.
+constexpr int kHalfPitch = 528, kWeightPitch = 2 * kHalfPitch, kRowPitch = 544;
+constexpr int kScaleBytes = 4 * kWeightPitch + 4 * kRowPitch;
+constexpr int kCopyWarp0 = 4, kEpi0 = 8, kEpiWarps = 8;
 constexpr int kWarps = kEpi0 + kEpiWarps, kThreads = kWarps * 32;
 // Registers a thread, of the kLaunchRegs that the block starts with: the
-// epilogue holds 128 accumulators.  Three shares of a warpgroup each (of four
-// warps), and no more in all than the block has.
-constexpr int kLaunchRegs = 128, kIssueRegs = 48, kScaleRegs = 96, kEpiRegs = 184;
-static_assert((kIssueRegs + kScaleRegs) * 128 + kEpiRegs * 256 <= kLaunchRegs * kThreads,
+// epilogue holds 128 accumulators.  Shares of a warpgroup each (of four warps),
+// and no more in all than the block has.
+constexpr int kLaunchRegs = 128, kIssueRegs = 40, kCopyRegs = 72, kEpiRegs = 200;
+static_assert((kIssueRegs + kCopyRegs) * 128 + kEpiRegs * 256 <= kLaunchRegs * kThreads,
               "registers");
 constexpr int kInfos = 4;                  // tiles looked up ahead
 constexpr int kFewRows = 32;               // rows that are columns
@@ -75,13 +80,13 @@ struct ProductArgs {
   const int32_t *offsets, *sti;
   const uint8_t *wscale[2];  // [E][R][K / 16] of the two tiles' matrices
   const float *wglobal[2];   // [E]
-  const uint8_t *xscale;     // [rows][K / 16]
+  const uint8_t *xcodes, *xscale;   // [rows][K / 2], [rows][K / 16]
   const float *xglobal;      // [rows]
   void *out;                 // [num_rows][R]
   uint32_t *err;
 };
 
-// Codes {K / 2 bytes, E * R rows} box {128, 128}; rows {K / 2, rows} box {128, 1}.
+// Codes {K / 2 bytes, E * R rows} box {128, 128}; rows {K / 2, rows} box {128, 32}.
 struct ProductMaps {
   CUtensorMap w[2], x;
 };
@@ -95,9 +100,9 @@ struct TileInfo {
 
 struct Smem {
   alignas(1024) uint8_t codes[kStages][kStageBytes];
-  alignas(16) uint8_t scales[kStages][3 * kScales];
+  alignas(16) uint8_t scales[kStages][kScaleBytes];
   alignas(16) TileInfo info[kInfos];
-  uint64_t full[kStages], empty[kStages], copied[kStages];
+  uint64_t full[kStages], empty[kStages];
   uint64_t info_full[kInfos], info_empty[kInfos];
   uint64_t acc_full, acc_empty, drain;
   int failed;
@@ -138,39 +143,30 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
         "=r"(r[31])
       : "r"(taddr));
 }
-// 16 or 32 consecutive 32-bit columns of this warp's 32 TMEM lanes, from registers.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+// One lane of a converged warp, the same one every time.  MMAs and copies are
+// issued under it and unrolled: the compiler knows of it that one lane is
+// active, and keeps descriptors in uniform registers.  (Under lane == 0 every
+// issue took 180 clocks, with it in a rolled loop 150; unrolled an MMA of 256
+// columns takes the tensor cores' own 128, and a copy of scales beside it none.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
-      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16"
-      "};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
-      "r"(r[14]), "r"(r[15])
-      : "memory");
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
-      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
-      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32"
-      "};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
-      "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+// 32 lines of 16 bytes in shared memory (8 lines of 128 bytes together) to four
+// columns of tensor memory, the same in all four quarters of the lanes.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t smem) {
+  const uint64_t desc = (uint64_t)((smem & 0x3FFFF) >> 4) | ((uint64_t)(128 >> 4) << 32) |
+                        ((uint64_t)1 << 46);
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc));
 }
-// Rows r0..r3 (from column x) of a two-dimensional map, 128 bytes each, to dst.
-__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, int x, int r0,
-                                            int r1, int r2, int r3, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3),
-      "r"(smem_addr(bar))
-      : "memory");
+// Arrives at a barrier, which counts it, when this thread's copies so far have
+// landed.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
 }
 __device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x, int y,
                                        uint64_t *bar) {
@@ -290,11 +286,10 @@ __device__ void producer(const ProductArgs &a, const ProductMaps &maps, Smem &S)
   uint32_t s = 0;
   Tiles tiles(S);
   while (const TileInfo *t = tiles.next()) {
-    const int rows = t->rows, m = t->m, w0 = t->e * a.R;
-    const int4 r4 = *reinterpret_cast<const int4 *>(&t->row[4 * lane]);
+    const int boxes = a.by_token ? 0 : (t->rows + 31) / 32, m = t->m, w0 = t->e * a.R, p0 = t->p0;
     tiles.done();
     const bool two = second_half<kPair>(a, m);
-    const uint32_t bytes = (two ? 2 : 1) * kOperand + (rows + 3) / 4 * 512;
+    const uint32_t bytes = (two ? 2 : 1) * kOperand + boxes * (32 * 128);
     for (int kb = 0; kb < kbs; ++kb, ++s) {
       const int slot = s % kStages;
       uint64_t *bar = &S.full[slot];
@@ -308,11 +303,10 @@ __device__ void producer(const ProductArgs &a, const ProductMaps &maps, Smem &S)
         tma_2d(dst, &maps.w[0], kb * 128, w0 + feature_of<kPair>(m, 0), bar);
         if (two)
           tma_2d(dst + kOperand, &maps.w[1], kb * 128, w0 + feature_of<kPair>(m, 1), bar);
+        for (int i = 0; i < boxes; ++i)
+          tma_2d(dst + 2 * kOperand + i * (32 * 128), &maps.x, kb * 128, p0 + 32 * i, bar);
       }
       __syncwarp();
-      if (4 * lane < rows)
-        tma_gather4(dst + 2 * kOperand + lane * 512, &maps.x, kb * 128, max(r4.x, 0),
-                    max(r4.y, 0), max(r4.z, 0), max(r4.w, 0), bar);
     }
     if (!tiles.ok) break;
   }
@@ -322,6 +316,47 @@ __device__ void producer(const ProductArgs &a, const ProductMaps &maps, Smem &S)
     const uint64_t t0 = gtime();
     while (!mbar_poll(&S.full[j % kStages], (j / kStages) & 1))
       if (gtime() - t0 > kWaitNs) break;
+  }
+}
+
+// The tensor cores' work on a stage: its scales to tensor memory, then a step of
+// 64 k (32 bytes of the swizzled rows) at a time.  kFew: the weights' halves are
+// the lanes and the tile's rows the columns; else the other way round.
+template <bool kFew, bool kTwo>
+__device__ __forceinline__ void issue_step(int i, uint32_t tmem, uint32_t sc, uint64_t w,
+                                           uint64_t x, uint32_t id, uint32_t acc) {
+  const uint32_t sw = sc + 8 * i, sx = sc + kRowScales + 4 * i;
+  if constexpr (kFew) {
+    mma_nvf4(tmem, w + 2 * i, x + 2 * i, id, sw, sx, acc);
+    if constexpr (kTwo)
+      mma_nvf4(tmem + kTileCols, w + (kOperand >> 4) + 2 * i, x + 2 * i, id, sw + 4, sx, acc);
+  } else {
+    mma_nvf4(tmem, x + 2 * i, w + 2 * i, id, sx, sw, acc);
+  }
+}
+template <bool kTwo>
+__device__ __forceinline__ void copy_step(int i, uint32_t sc, uint32_t scales) {
+  tmem_copy_scales(sc + 8 * i, scales + i * kWeightPitch);
+  if constexpr (kTwo) tmem_copy_scales(sc + 8 * i + 4, scales + i * kWeightPitch + kHalfPitch);
+  tmem_copy_scales(sc + kRowScales + 4 * i, scales + 4 * kWeightPitch + i * kRowPitch);
+}
+template <bool kFew, bool kTwo>
+__device__ __forceinline__ void issue_stage(Smem &S, int slot, uint32_t tmem, uint32_t id,
+                                            int steps, bool first) {
+  const uint32_t codes = smem_addr(S.codes[slot]), scales = smem_addr(S.scales[slot]);
+  const uint64_t w = sdesc(codes), x = sdesc(codes + 2 * kOperand);
+  const uint32_t sc = tmem + kScaleBase + slot * kScaleCols;
+  if (steps == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) copy_step<kTwo>(i, sc, scales);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      issue_step<kFew, kTwo>(i, tmem, sc, w, x, id, i || !first);
+  } else {
+    for (int i = 0; i < steps; ++i) {
+      copy_step<kTwo>(i, sc, scales);
+      issue_step<kFew, kTwo>(i, tmem, sc, w, x, id, i || !first);
+    }
   }
 }
 
@@ -347,22 +382,18 @@ __device__ void mma_issuer(const ProductArgs &a, Smem &S, uint32_t tmem) {
         break;
       }
       tc_fence_after();
-      if (lane == 0) {
-        const int steps = min(4, (a.K - kb * 256 + 63) / 64);   // 64 k: 32 bytes of the row
-        const uint32_t codes = smem_addr(S.codes[slot]);
-        const uint64_t w = sdesc(codes), x = sdesc(codes + 2 * kOperand);
-        const uint32_t sc = tmem + kScaleBase + slot * kScaleCols;
-        for (int i = 0; i < steps; ++i) {
-          const uint32_t acc = (kb | i) != 0, sx = sc + kRowScales + 4 * i;
-          if (few) {
-            mma_nvf4(tmem, w + 2 * i, x + 2 * i, id, sc + 8 * i, sx, acc);
-            if (two)
-              mma_nvf4(tmem + kTileCols, w + (kOperand >> 4) + 2 * i, x + 2 * i, id,
-                       sc + 8 * i + 4, sx, acc);
-          } else {
-            mma_nvf4(tmem, x + 2 * i, w + 2 * i, id, sx, sc + 8 * i, acc);
-          }
-        }
+      const int steps = min(4, (a.K - kb * 256 + 63) / 64);
+      if (elect_one()) {
+        // what other threads' cp.async wrote, ahead of the tensor cores' reads
+        fence_proxy_async_smem();
+        if (few && two)
+          issue_stage<true, true>(S, slot, tmem, id, steps, kb == 0);
+        else if (few)
+          issue_stage<true, false>(S, slot, tmem, id, steps, kb == 0);
+        else if (two)
+          issue_stage<false, true>(S, slot, tmem, id, steps, kb == 0);
+        else
+          issue_stage<false, false>(S, slot, tmem, id, steps, kb == 0);
         mma_commit(&S.empty[slot]);
         if (kb == kbs - 1) mma_commit(&S.acc_full);
       }
@@ -372,7 +403,7 @@ __device__ void mma_issuer(const ProductArgs &a, Smem &S, uint32_t tmem) {
   }
   if (!tiles.ok && lane == 0) fail(S, a);
   // tensor memory is given back only after the last MMA
-  if (lane == 0) {
+  if (elect_one()) {
     mma_commit(&S.drain);
     const uint64_t t0 = gtime();
     while (!mbar_poll(&S.drain, 0))
@@ -381,125 +412,93 @@ __device__ void mma_issuer(const ProductArgs &a, Smem &S, uint32_t tmem) {
   __syncwarp();
 }
 
-// Copies the scales of 16 blocks (those ahead of K) of one row to shared
-// memory, zeros for the rest: by 16 or 4 bytes asynchronously (ALIGN: of the
-// rows' scales), else by two through registers.
-template <int ALIGN>
-__device__ __forceinline__ void copy_scales(uint8_t *dst, const uint8_t *row, int first, int have) {
-  // have: blocks of the row behind `first`, <= 0 for no row
-  if constexpr (ALIGN == 16) {
-    const bool there = have > 0;   // whole pieces: K is a multiple of 256
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)),
-                 "l"(there ? row + first : row), "r"(there ? 16 : 0)
-                 : "memory");
-  } else if constexpr (ALIGN == 4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      copy_async<4>(smem_addr(dst + 4 * i), 4 * i < have ? row + first + 4 * i : row,
-                    4 * i < have);
+// Copies the word of 4 blocks' scales at p, of which `have` are in the row (0 or
+// less: none), zeros for the others: asynchronously where rows of scales are
+// whole words (kWords), else through registers, by two.
+template <bool kWords>
+__device__ __forceinline__ void copy_word(uint8_t *dst, const uint8_t *p, const uint8_t *any,
+                                          int have) {
+  if constexpr (kWords) {
+    copy_async<4>(smem_addr(dst), have > 0 ? p : any, have > 0);
   } else {
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (2 * i < have)
-        w[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t *>(row + first + 2 * i)
-                    << (16 * (i & 1));
-    *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    uint32_t w = 0;
+    if (have > 0) w = *reinterpret_cast<const uint16_t *>(p);
+    if (have > 2) w |= (uint32_t)*reinterpret_cast<const uint16_t *>(p + 2) << 16;
+    *reinterpret_cast<uint32_t *>(dst) = w;
   }
 }
 
-// Walks over the stages of a CTA's tiles, one copy of scales at a time.
-template <bool kPair, int ALIGN>
-struct ScaleWalk {
-  const ProductArgs &a;
-  Smem &S;
-  Tiles tiles;
-  int kb, kbs, thread;
-  bool end = false;
-  uint32_t issued = 0;
-  const uint8_t *row[3];   // this thread's rows of the tile's operands, NULL: none
-
-  __device__ __forceinline__ ScaleWalk(const ProductArgs &args, Smem &sm)
-      : a(args), S(sm), tiles(sm), kb((args.K + 255) / 256), kbs(kb),
-        thread((int)threadIdx.x - kScaleWarp0 * 32) {}
-  // The next stage's copies (one group, empty behind the end).
-  __device__ __forceinline__ void next() {
-    if (kb == kbs && !end) {
-      if (const TileInfo *t = tiles.next()) {
-        const int pitch = a.K / 16;
+// Warps 4-7.  Scales: a thread has one step of 64 k (its lane % 4), so that four
+// lanes read 16 neighbouring bytes of a row, and 4 rows of each operand's 128.
+// Tokens' rows: eight lanes have a row's 128 bytes; the 16-byte piece c of row r
+// goes to c ^ (r % 8), as the swizzle has it.
+template <bool kPair, bool kWords>
+__device__ void copier(const ProductArgs &a, Smem &S) {
+  const int warp = (threadIdx.x >> 5) - kCopyWarp0, lane = threadIdx.x & 31;
+  const int step = lane & 3, j = (lane >> 2) & 3, line = (lane >> 4) + 8 * warp;   // and + 2, 4, 6
+  const int first = 32 * j + line;
+  const int piece = lane & 7, row0 = 4 * warp + (lane >> 3);   // and + 16, 32, ...
+  const int pitch = a.K / 16, kbs = (a.K + 255) / 256;
+  uint32_t s = 0;
+  Tiles tiles(S);
+  while (const TileInfo *t = tiles.next()) {
+    const int rows = t->rows;
+    const uint8_t *w[2];
+    int left[2], xs[4], xc[8];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int f = feature_of<kPair>(t->m, j) + thread;
-          row[j] = f < a.R ? a.wscale[j] + ((int64_t)t->e * a.R + f) * pitch : nullptr;
-        }
-        const int x = t->row[thread];
-        row[2] = x >= 0 ? a.xscale + (int64_t)x * pitch : nullptr;
-        tiles.done();
-        kb = 0;
-      } else {
-        end = true;
+    for (int h = 0; h < 2; ++h) {
+      const int f = feature_of<kPair>(t->m, h) + first;
+      w[h] = a.wscale[h] + ((int64_t)t->e * a.R + f) * pitch + 4 * step;
+      left[h] = a.R - f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) xs[i] = t->row[first + 2 * i];
+    if (a.by_token) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) xc[i] = row0 + 16 * i < rows ? t->row[row0 + 16 * i] : -1;
+    }
+    tiles.done();
+    for (int kb = 0; kb < kbs; ++kb, ++s) {
+      const int slot = s % kStages, have = pitch - 16 * kb - 4 * step;
+      if (s >= kStages && !wait_all(S, &S.empty[slot], (s / kStages - 1) & 1)) {
+        tiles.ok = false;
+        break;
       }
-    }
-    if (kb < kbs) {
-      uint8_t *dst = S.scales[issued % kStages] + thread * 16;
+      if (a.by_token) {
+        const int at = kb * 128 + piece * 16, len = a.K / 2;
+        const uint32_t dst = smem_addr(S.codes[slot]) + 2 * kOperand + row0 * 128 +
+                             ((piece ^ (row0 & 7)) << 4);
 #pragma unroll
-      for (int j = 0; j < 3; ++j)
-        copy_scales<ALIGN>(dst + j * kScales, row[j] ? row[j] : a.wscale[0], row[j] ? kb * 16 : 0,
-                           row[j] ? a.K / 16 - kb * 16 : 0);
-      ++kb;
-      ++issued;
+        for (int i = 0; i < 8; ++i)
+          if (xc[i] >= 0) {
+            const uint8_t *p = a.xcodes + (int64_t)xc[i] * len;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 2048),
+                         "l"(at < len ? p + at : p), "r"(at < len ? 16 : 0)
+                         : "memory");
+          }
+      }
+      uint8_t *dst = S.scales[slot] + line * 16 + j * 4;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          copy_word<kWords>(dst + step * kWeightPitch + h * kHalfPitch + i * 32,
+                            w[h] + (int64_t)(2 * i) * pitch + 16 * kb, a.wscale[0],
+                            2 * i < left[h] ? have : 0);
+      if (32 * j < rows) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          copy_word<kWords>(dst + 4 * kWeightPitch + step * kRowPitch + i * 32,
+                            a.xscale + (int64_t)xs[i] * pitch + 4 * step + 16 * kb, a.wscale[0],
+                            xs[i] >= 0 ? have : 0);
+      }
+      // the copies' own arrival, and this thread's for what it stored itself
+      copies_arrive(&S.full[slot]);
+      if constexpr (!kWords) mbar_arrive(&S.full[slot]);
     }
-    copies_commit();
+    if (!tiles.ok) break;
   }
-};
-
-// Warps 4-7.  Shared memory is a ring that these warps alone use: a slot is
-// written again by the copies of stage s + 3, which are started once all four
-// have met at stage s, each after it has read stage s - 1.
-template <bool kPair, int ALIGN>
-__device__ void scale_role(const ProductArgs &a, Smem &S, uint32_t tmem) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kScaleBase;
-  ScaleWalk<kPair, ALIGN> walk(a, S);
-  for (int d = 0; d < kStages - 1; ++d) walk.next();
-  bool ok = true;
-  for (uint32_t s = 0; s < walk.issued; ++s) {
-    const int slot = s % kStages;
-    copies_wait(kStages - 1);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&S.copied[slot]);
-    ok = wait_all(S, &S.copied[slot], (s / kStages) & 1);
-    if (!ok) break;
-    uint32_t w[32], x[16];   // column 8 i + 4 half + row / 32 of step i, and 4 i + row / 32
-    const uint8_t *from = S.scales[slot] + lane * 16;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const uint4 v = *reinterpret_cast<const uint4 *>(from + q * 512);
-      w[q] = v.x;
-      w[8 + q] = v.y;
-      w[16 + q] = v.z;
-      w[24 + q] = v.w;
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint4 v = *reinterpret_cast<const uint4 *>(from + 2 * kScales + q * 512);
-      x[q] = v.x;
-      x[4 + q] = v.y;
-      x[8 + q] = v.z;
-      x[12 + q] = v.w;
-    }
-    walk.next();
-    if (s >= kStages) ok = wait_all(S, &S.empty[slot], (s / kStages - 1) & 1);
-    if (!ok) break;
-    tc_fence_after();
-    tmem_st32(base + slot * kScaleCols, w);
-    tmem_st16(base + slot * kScaleCols + kRowScales, x);
-    tmem_wait_st();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&S.full[slot]);
-  }
-  if ((!ok || !walk.tiles.ok) && lane == 0) fail(S, a);
+  if (!tiles.ok && lane == 0) fail(S, a);
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
@@ -637,7 +636,7 @@ __device__ void epilogue(const ProductArgs &a, Smem &S, uint32_t tmem) {
   if (!tiles.ok && lane == 0) fail(S, a);
 }
 
-template <typename T, bool kPair, int ALIGN>
+template <typename T, bool kPair, bool kWords>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_nvfp4_kernel(const __grid_constant__ ProductArgs a,
                          const __grid_constant__ ProductMaps maps) {
@@ -646,13 +645,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&S.full[i], 1 + kScaleWarps);   // the copies, and each scale warp
+      // the TMA copies, and every thread of the copying warps (twice: copier)
+      mbar_init(&S.full[i], 1 + 128 * (kWords ? 1 : 2));
       mbar_init(&S.empty[i], 1);
-      mbar_init(&S.copied[i], kScaleWarps);
     }
     for (int i = 0; i < kInfos; ++i) {
       mbar_init(&S.info_full[i], 1);
-      mbar_init(&S.info_empty[i], 2 + kScaleWarps + kEpiWarps);
+      mbar_init(&S.info_empty[i], 2 + 4 + kEpiWarps);
     }
     mbar_init(&S.acc_full, 1);
     mbar_init(&S.acc_empty, kEpiWarps);
@@ -711,9 +710,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kEpi0) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     epilogue<T, kPair>(a, S, tmem);
-  } else if (warp >= kScaleWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kScaleRegs));
-    scale_role<kPair, ALIGN>(a, S, tmem);
+  } else if (warp >= kCopyWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+    copier<kPair, kWords>(a, S);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == 0)
@@ -793,6 +792,7 @@ int grouped(const moe_proj *w0, const moe_proj *w1, int E, int R, int K, const u
     a.wscale[j] = static_cast<const uint8_t *>(w[j]->scale);
     a.wglobal[j] = w[j]->global_scale;
   }
+  a.xcodes = codes;
   a.xscale = scale;
   a.xglobal = global;
   a.out = out;
@@ -804,7 +804,7 @@ int grouped(const moe_proj *w0, const moe_proj *w1, int E, int R, int K, const u
   const cuuint64_t pitch[1] = {(cuuint64_t)K / 2};
   const cuuint64_t wd[2] = {(cuuint64_t)K / 2, (cuuint64_t)E * R};
   const cuuint64_t xd[2] = {(cuuint64_t)K / 2, (cuuint64_t)(by_token ? M : num_rows)};
-  const cuuint32_t wbox[2] = {128, 128}, xbox[2] = {128, 1};
+  const cuuint32_t wbox[2] = {128, 128}, xbox[2] = {128, 32};
   for (int j = 0; j < 2; ++j)
     if (const int st = encode_u8_sw128(&maps.w[j], w[j]->codes, 2, wd, pitch, wbox)) return st;
   if (const int st = encode_u8_sw128(&maps.x, codes, 2, xd, pitch, xbox)) return st;
@@ -821,9 +821,8 @@ int grouped(const moe_proj *w0, const moe_proj *w1, int E, int R, int K, const u
       if (const int st = ensure_registers((const void *)kernel)) return st;
       return launch_pdl(kernel, grid, dim3(kThreads), kSmemBytes, stream, a, maps);
     };
-    if (K % 256 == 0) return launch(grouped_nvfp4_kernel<T, P, 16>);
-    if (K % 64 == 0) return launch(grouped_nvfp4_kernel<T, P, 4>);
-    return launch(grouped_nvfp4_kernel<T, P, 2>);
+    if (K % 64 == 0) return launch(grouped_nvfp4_kernel<T, P, true>);
+    return launch(grouped_nvfp4_kernel<T, P, false>);
   };
   auto typed = [&](auto pair) {
     switch (dtype) {
