@@ -25,17 +25,20 @@
 //    place them as the swizzle would, so that tokens need not be copied into
 //    expert order first.  (TMA gathers of four rows each took the gate and up
 //    of 4096 rows from 91 to 150 us.)
-//  * Scales stay row-major as the format has them.  They are copied by
-//    words (4 blocks, 64 k) to where the tensor cores' own copy to tensor
-//    memory takes them (tcgen05.cp 32x128b, issued ahead of the stage's MMAs):
-//    for each 64 k and 128 rows 32 x 16 bytes, line = row % 32, word = row / 32.
+//  * Scales stay row-major as the format has them.  TMA brings a stage's 16
+//    bytes a row, and four warps turn them by words of 4 blocks (64 k) to where
+//    the tensor cores' own copy to tensor memory takes them (tcgen05.cp 32x128b,
+//    issued ahead of the stage's MMAs): for each 64 k and 128 rows 32 x 16 bytes,
+//    line = row % 32, word = row / 32.  Rows of scales that TMA does not take (k
+//    no multiple of 256) the four warps copy there by words.
 //  * A persistent CTA an SM walks over (expert, feature tile, row tile), the
 //    row tiles innermost: CTAs next to one another share weights, and an
 //    expert's rows stay in L2.
-//  * Roles: warp 0 copies, warp 1 issues MMAs, warp 2 looks the tiles up ahead
-//    of all others, warps 4-7 bring the scales and tokens' rows, warps 8-15 the epilogue, which
-//    takes the accumulators into registers first, so that the next tile's MMAs
-//    run beside its arithmetic and stores.  The roles meet at mbarriers alone;
+//  * Roles: warp 0 starts the copies of codes and warp 3 those of scales, which
+//    run further ahead, warp 1 issues MMAs, warp 2 looks the tiles up ahead of
+//    all others, warps 4-7 turn the scales and copy tokens' rows, warps 8-15 are
+//    the epilogue, which takes the accumulators into registers first, so that
+//    the next tile's MMAs run beside its arithmetic and stores.  The roles meet at mbarriers alone;
 //    every wait gives up after about two seconds with MOE_ERR_TIMEOUT.
 #include <cstring>
 
@@ -48,14 +51,16 @@ namespace {
 using namespace tc;
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kTileRows = 128;             // rows of a row tile, features of a feature tile
 constexpr int kOperand = 128 * 128;        // bytes of a stage's codes of 128 rows
 constexpr int kStageBytes = 3 * kOperand;  // two weight tiles, the rows
 // The scales of a stage in shared memory: 512 bytes for each 64 k and 128 rows,
-// set apart so that a warp's words of 8 rows x 4 steps lie in 32 banks.
+// set apart so that a warp's words of 8 rows x 4 steps, or pieces of 2 x 4, lie in
+// 32 banks.
 constexpr int kHalfPitch = 528, kWeightPitch = 2 * kHalfPitch, kRowPitch = 544;
 constexpr int kScaleBytes = 4 * kWeightPitch + 4 * kRowPitch;
+constexpr int kRawScales = 128 * 16;   // of 128 rows, row by row
 constexpr int kCopyWarp0 = 4, kEpi0 = 8, kEpiWarps = 8;
 constexpr int kWarps = kEpi0 + kEpiWarps, kThreads = kWarps * 32;
 // Registers a thread, of the kLaunchRegs that the block starts with: the
@@ -75,7 +80,8 @@ struct ProductArgs {
   int E, R, K;               // experts, output features, input features
   int by_token, top_k, n;    // n slots
   int num_rows;              // of the expert-order buffers
-  int align;                 // of the output's rows, in bytes: 32, 16 or less
+  int x_rows;                // of the rows' codes and scales
+  int align;                 // of the output's rows, in bytes: 16 or less
   int feature_tiles;         // pairs of tiles (or gate and up tiles) of an expert
   const int32_t *offsets, *sti;
   const uint8_t *wscale[2];  // [E][R][K / 16] of the two tiles' matrices
@@ -86,9 +92,11 @@ struct ProductArgs {
   uint32_t *err;
 };
 
-// Codes {K / 2 bytes, E * R rows} box {128, 128}; rows {K / 2, rows} box {128, 32}.
+// Codes {K / 2 bytes, E * R rows} box {128, 128} (pairs of matrices) or {128, 256};
+// rows {K / 2, rows} box {128, 32} and {128, 128}; scales {K / 16 bytes, E * R rows}
+// and {K / 16, rows} with 16 bytes of as many rows.
 struct ProductMaps {
-  CUtensorMap w[2], x;
+  CUtensorMap w[2], x[2], ws[2], xs;
 };
 
 // A tile as every role reads it; rows < 0: no more tiles.
@@ -100,9 +108,11 @@ struct TileInfo {
 
 struct Smem {
   alignas(1024) uint8_t codes[kStages][kStageBytes];
+  alignas(128) uint8_t raw[kStages][3 * kRawScales];   // scales by row, as TMA brings them
   alignas(16) uint8_t scales[kStages][kScaleBytes];
+  alignas(128) uint8_t staged[kEpiWarps][32 * 128];    // output on its way out, a warp's own
   alignas(16) TileInfo info[kInfos];
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kStages], empty[kStages], raw_full[kStages], raw_empty[kStages];
   uint64_t info_full[kInfos], info_empty[kInfos];
   uint64_t acc_full, acc_empty, drain;
   int failed;
@@ -187,8 +197,18 @@ __device__ __forceinline__ void fail(Smem &S, const ProductArgs &a) {
   *(volatile int *)&S.failed = 1;
   if (a.err) atomicOr(a.err, MOE_ERR_TIMEOUT);
 }
+// A whole warp's wait for a phase.  The barrier's own waiting test parks the warp
+// for a while; the clock and the other roles' failure are looked at now and then.
 __device__ __forceinline__ bool wait_all(Smem &S, uint64_t *bar, uint32_t parity) {
-  return __all_sync(kFull, wait_phase(&S.failed, bar, parity));
+  bool ok = mbar_try(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = gtime();
+    for (uint32_t i = 1; i < (1u << 28); ++i) {
+      ok = mbar_try(bar, parity);
+      if (ok || ((i & 63) == 0 && (*(volatile int *)&S.failed || gtime() - t0 > kWaitNs))) break;
+    }
+  }
+  return __all_sync(kFull, ok);
 }
 
 // Warp 2: the CTA's tiles in order, without those of padding alone.
@@ -280,43 +300,80 @@ __device__ __forceinline__ int feature_of(int m, int j) {
   return kPair ? m * 128 : m * 256 + j * 128;
 }
 
+// Waits until the copies counted by the last stages of a ring of barriers have
+// landed: none may be in flight when the CTA ends.
+__device__ __forceinline__ void copies_drain(uint64_t *bars, uint32_t s) {
+  for (uint32_t j = s < kStages ? 0 : s - kStages; j < s; ++j) {
+    const uint64_t t0 = gtime();
+    while (!mbar_poll(&bars[j % kStages], (j / kStages) & 1))
+      if (gtime() - t0 > kWaitNs) break;
+  }
+}
+
+// Warp 0: codes of the weights, and of rows in expert order.
 template <bool kPair>
 __device__ void producer(const ProductArgs &a, const ProductMaps &maps, Smem &S) {
-  const int lane = threadIdx.x & 31, kbs = (a.K + 255) / 256;
+  const int kbs = (a.K + 255) / 256;
   uint32_t s = 0;
   Tiles tiles(S);
   while (const TileInfo *t = tiles.next()) {
-    const int boxes = a.by_token ? 0 : (t->rows + 31) / 32, m = t->m, w0 = t->e * a.R, p0 = t->p0;
+    const int rows = a.by_token ? 0 : t->rows <= 32 ? 32 : 128, p0 = t->p0;
+    const int w0 = t->e * a.R + feature_of<kPair>(t->m, 0);
     tiles.done();
-    const bool two = second_half<kPair>(a, m);
-    const uint32_t bytes = (two ? 2 : 1) * kOperand + boxes * (32 * 128);
+    const uint32_t bytes = 2 * kOperand + rows * 128;
+    const CUtensorMap *x = &maps.x[rows == 128];
     for (int kb = 0; kb < kbs; ++kb, ++s) {
       const int slot = s % kStages;
-      uint64_t *bar = &S.full[slot];
       if (s >= kStages && !wait_all(S, &S.empty[slot], (s / kStages - 1) & 1)) {
         tiles.ok = false;
         break;
       }
-      uint8_t *dst = S.codes[slot];
-      if (lane == 0) {
+      if (elect_one()) {
+        uint64_t *bar = &S.full[slot];
+        uint8_t *dst = S.codes[slot];
         mbar_expect_tx(bar, bytes);
-        tma_2d(dst, &maps.w[0], kb * 128, w0 + feature_of<kPair>(m, 0), bar);
-        if (two)
-          tma_2d(dst + kOperand, &maps.w[1], kb * 128, w0 + feature_of<kPair>(m, 1), bar);
-        for (int i = 0; i < boxes; ++i)
-          tma_2d(dst + 2 * kOperand + i * (32 * 128), &maps.x, kb * 128, p0 + 32 * i, bar);
+        tma_2d(dst, &maps.w[0], kb * 128, w0, bar);
+        if constexpr (kPair) tma_2d(dst + kOperand, &maps.w[1], kb * 128, w0, bar);
+        if (rows) tma_2d(dst + 2 * kOperand, x, kb * 128, p0, bar);
       }
       __syncwarp();
     }
     if (!tiles.ok) break;
   }
-  if (!tiles.ok && lane == 0) fail(S, a);
-  // no copy may be in flight when the CTA ends
-  for (uint32_t j = s < kStages ? 0 : s - kStages; j < s; ++j) {
-    const uint64_t t0 = gtime();
-    while (!mbar_poll(&S.full[j % kStages], (j / kStages) & 1))
-      if (gtime() - t0 > kWaitNs) break;
+  if (!tiles.ok && (threadIdx.x & 31) == 0) fail(S, a);
+  copies_drain(S.full, s);
+}
+
+// Warp 3: their scales, row by row.
+template <bool kPair>
+__device__ void scale_producer(const ProductArgs &a, const ProductMaps &maps, Smem &S) {
+  const int kbs = a.K / 256;
+  const uint32_t bytes = (a.by_token ? 2 : 3) * kRawScales;
+  uint32_t s = 0;
+  Tiles tiles(S);
+  while (const TileInfo *t = tiles.next()) {
+    const int w0 = t->e * a.R + feature_of<kPair>(t->m, 0), p0 = t->p0;
+    tiles.done();
+    for (int kb = 0; kb < kbs; ++kb, ++s) {
+      const int slot = s % kStages;
+      if (s >= kStages && !wait_all(S, &S.raw_empty[slot], (s / kStages - 1) & 1)) {
+        tiles.ok = false;
+        break;
+      }
+      if (elect_one()) {
+        uint64_t *bar = &S.raw_full[slot];
+        uint8_t *dst = S.raw[slot];
+        mbar_expect_tx(bar, bytes);
+        tma_2d(dst, &maps.ws[0], kb * 16, w0, bar);
+        if constexpr (kPair) tma_2d(dst + kRawScales, &maps.ws[1], kb * 16, w0, bar);
+        if (!a.by_token) tma_2d(dst + 2 * kRawScales, &maps.xs, kb * 16, p0, bar);
+      }
+      __syncwarp();
+    }
+    if (!tiles.ok) break;
   }
+  if (!tiles.ok && (threadIdx.x & 31) == 0) fail(S, a);
+  copies_drain(S.raw_full, s);
 }
 
 // The tensor cores' work on a stage: its scales to tensor memory, then a step of
@@ -412,89 +469,228 @@ __device__ void mma_issuer(const ProductArgs &a, Smem &S, uint32_t tmem) {
   __syncwarp();
 }
 
-// Copies the word of 4 blocks' scales at p, of which `have` are in the row (0 or
-// less: none), zeros for the others: asynchronously where rows of scales are
-// whole words (kWords), else through registers, by two.
-template <bool kWords>
-__device__ __forceinline__ void copy_word(uint8_t *dst, const uint8_t *p, const uint8_t *any,
-                                          int have) {
-  if constexpr (kWords) {
-    copy_async<4>(smem_addr(dst), have > 0 ? p : any, have > 0);
-  } else {
-    uint32_t w = 0;
-    if (have > 0) w = *reinterpret_cast<const uint16_t *>(p);
-    if (have > 2) w |= (uint32_t)*reinterpret_cast<const uint16_t *>(p + 2) << 16;
-    *reinterpret_cast<uint32_t *>(dst) = w;
+// Tokens' rows of a stage: eight lanes have a row's 128 bytes; the 16-byte piece c
+// of row r goes to c ^ (r % 8), as the swizzle has it.  places: of the rows 4 warp
+// + lane / 8 + 16 i, in pieces from the codes' beginning; ~0: none.
+__device__ __forceinline__ void row_places(const ProductArgs &a, const TileInfo &t, int row0,
+                                           uint32_t (&places)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int x = t.row[row0 + 16 * i];
+    places[i] = x >= 0 ? (uint32_t)x * (uint32_t)(a.K / 32) : ~0u;
   }
 }
+__device__ __forceinline__ void copy_rows(const ProductArgs &a, uint8_t *dst, int row0, int kb,
+                                          const uint32_t (&places)[8]) {
+  const int piece = threadIdx.x & 7, from = kb * 128 + piece * 16, len = a.K / 2;
+  const uint8_t *src = a.xcodes + (from < len ? from : 0);
+  const uint32_t to = smem_addr(dst) + row0 * 128 + ((piece ^ (row0 & 7)) << 4);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (places[i] != ~0u)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * 2048),
+                   "l"(src + (uint64_t)places[i] * 16), "r"(from < len ? 16 : 0)
+                   : "memory");
+}
 
-// Warps 4-7.  Scales: a thread has one step of 64 k (its lane % 4), so that four
-// lanes read 16 neighbouring bytes of a row, and 4 rows of each operand's 128.
-// Tokens' rows: eight lanes have a row's 128 bytes; the 16-byte piece c of row r
-// goes to c ^ (r % 8), as the swizzle has it.
-template <bool kPair, bool kWords>
-__device__ void copier(const ProductArgs &a, Smem &S) {
+// Warps 4-7 with scales by TMA: a thread turns line = 8 warp + lane / 4 of step
+// lane % 4, the words of the rows line, line + 32, + 64, + 96, of each operand.
+// Tokens' scales come by a load for each row, a stage ahead.
+template <bool kPair>
+__device__ void turner(const ProductArgs &a, Smem &S) {
   const int warp = (threadIdx.x >> 5) - kCopyWarp0, lane = threadIdx.x & 31;
-  const int step = lane & 3, j = (lane >> 2) & 3, line = (lane >> 4) + 8 * warp;   // and + 2, 4, 6
-  const int first = 32 * j + line;
-  const int piece = lane & 7, row0 = 4 * warp + (lane >> 3);   // and + 16, 32, ...
-  const int pitch = a.K / 16, kbs = (a.K + 255) / 256;
+  const int line = 8 * warp + (lane >> 2), step = lane & 3;
+  const int row0 = 4 * warp + (lane >> 3);
+  const int pitch = a.K / 16, kbs = a.K / 256;
   uint32_t s = 0;
   Tiles tiles(S);
   while (const TileInfo *t = tiles.next()) {
-    const int rows = t->rows;
-    const uint8_t *w[2];
-    int left[2], xs[4], xc[8];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int f = feature_of<kPair>(t->m, h) + first;
-      w[h] = a.wscale[h] + ((int64_t)t->e * a.R + f) * pitch + 4 * step;
-      left[h] = a.R - f;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) xs[i] = t->row[first + 2 * i];
+    const int words = (t->rows + 31) / 32;
+    uint32_t places[8];
+    const uint8_t *own = nullptr;   // the scales of row line + 32 step: words `step` of its line
+    uint4 ahead = make_uint4(0, 0, 0, 0);
     if (a.by_token) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) xc[i] = row0 + 16 * i < rows ? t->row[row0 + 16 * i] : -1;
+      row_places(a, *t, row0, places);
+      const int x = t->row[line + 32 * step];
+      if (x >= 0) {
+        own = a.xscale + (int64_t)x * pitch;
+        ahead = *reinterpret_cast<const uint4 *>(own);
+      }
     }
     tiles.done();
     for (int kb = 0; kb < kbs; ++kb, ++s) {
-      const int slot = s % kStages, have = pitch - 16 * kb - 4 * step;
+      const int slot = s % kStages;
+      const uint4 x = ahead;
+      if (own && kb + 1 < kbs) ahead = *reinterpret_cast<const uint4 *>(own + 16 * kb + 16);
       if (s >= kStages && !wait_all(S, &S.empty[slot], (s / kStages - 1) & 1)) {
         tiles.ok = false;
         break;
       }
       if (a.by_token) {
-        const int at = kb * 128 + piece * 16, len = a.K / 2;
-        const uint32_t dst = smem_addr(S.codes[slot]) + 2 * kOperand + row0 * 128 +
-                             ((piece ^ (row0 & 7)) << 4);
+        copy_rows(a, S.codes[slot] + 2 * kOperand, row0, kb, places);
+        copies_arrive(&S.full[slot]);
+      }
+      if (!wait_all(S, &S.raw_full[slot], (s / kStages) & 1)) {
+        tiles.ok = false;
+        break;
+      }
+      const uint8_t *from = S.raw[slot] + line * 16 + step * 4;
+      uint8_t *to = S.scales[slot] + line * 16;
+      auto turn = [&](const uint8_t *p, uint8_t *q) {
+        uint4 v;
+        v.x = *reinterpret_cast<const uint32_t *>(p);
+        v.y = *reinterpret_cast<const uint32_t *>(p + 512);
+        v.z = *reinterpret_cast<const uint32_t *>(p + 1024);
+        v.w = *reinterpret_cast<const uint32_t *>(p + 1536);
+        *reinterpret_cast<uint4 *>(q) = v;
+      };
+      turn(from, to + step * kWeightPitch);
+      turn(from + kRawScales, to + step * kWeightPitch + kHalfPitch);
+      uint8_t *xto = to + 4 * kWeightPitch;
+      if (!a.by_token) {
+        turn(from + 2 * kRawScales, xto + step * kRowPitch);
+      } else if (step < words) {
+        *reinterpret_cast<uint32_t *>(xto + 4 * step) = x.x;
+        *reinterpret_cast<uint32_t *>(xto + 4 * step + kRowPitch) = x.y;
+        *reinterpret_cast<uint32_t *>(xto + 4 * step + 2 * kRowPitch) = x.z;
+        *reinterpret_cast<uint32_t *>(xto + 4 * step + 3 * kRowPitch) = x.w;
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&S.full[slot]);
+        mbar_arrive(&S.raw_empty[slot]);
+      }
+    }
+    if (!tiles.ok) break;
+  }
+  if (!tiles.ok && lane == 0) fail(S, a);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// The 16 bytes of a row's scales from byte `at` (even) of an array of `total` on,
+// `have` of them in the row (0 or less: none) and zeros behind, out of the two
+// aligned pieces around them.
+__device__ __forceinline__ uint4 load_scales(const uint8_t *base, int64_t at, int have,
+                                             int64_t total) {
+  const int64_t piece = at & ~(int64_t)15;
+  const int off = (int)(at & 15), need = off + min(have, 16);
+  uint32_t w[8];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    const int64_t p = piece + 16 * q;
+    if (have > 0 && 16 * q < need) {
+      if (p + 16 <= total) {
+        v = *reinterpret_cast<const uint4 *>(base + p);
+      } else {   // the array's last bytes
+        uint32_t b[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (xc[i] >= 0) {
-            const uint8_t *p = a.xcodes + (int64_t)xc[i] * len;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 2048),
-                         "l"(at < len ? p + at : p), "r"(at < len ? 16 : 0)
-                         : "memory");
-          }
+          if (p + 2 * i < total)
+            b[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t *>(base + p + 2 * i)
+                        << (16 * (i & 1));
+        v = make_uint4(b[0], b[1], b[2], b[3]);
       }
+    }
+    w[4 * q] = v.x;
+    w[4 * q + 1] = v.y;
+    w[4 * q + 2] = v.z;
+    w[4 * q + 3] = v.w;
+  }
+#pragma unroll
+  for (int d = 2; d > 0; d >>= 1) {
+    const bool down = off & (4 * d);
+#pragma unroll
+    for (int i = 0; i + d < 8; ++i) w[i] = down ? w[i + d] : w[i];
+  }
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
+    const int left = have - 4 * i;
+    v[i] = left >= 4 ? x : left < 2 ? 0 : x & 0xFFFFu;
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Warps 4-7 with scales of other widths.  Whole words (k a multiple of 64): a
+// thread copies those of one step of 64 k (its lane % 4), so that four lanes read
+// 16 neighbouring bytes of a row, of 4 rows of each operand's 128.  Else a thread
+// loads the 16 bytes of a row of each operand.
+template <bool kPair>
+__device__ void copier(const ProductArgs &a, Smem &S) {
+  const int warp = (threadIdx.x >> 5) - kCopyWarp0, lane = threadIdx.x & 31;
+  const bool words = a.K % 64 == 0;
+  // the step, word and line of what is stored first
+  const int step = words ? lane & 3 : 0, j = words ? (lane >> 2) & 3 : lane & 3;
+  const int line = words ? (lane >> 4) + 8 * warp : 8 * warp + (lane >> 2);
+  const int first = 32 * j + line, row0 = 4 * warp + (lane >> 3);
+  const int pitch = a.K / 16, kbs = (a.K + 255) / 256;
+  uint32_t s = 0;
+  Tiles tiles(S);
+  while (const TileInfo *t = tiles.next()) {
+    const int rows = t->rows;
+    int64_t w[2];
+    int left[2], xs[4];
+    uint32_t places[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int f = feature_of<kPair>(t->m, h) + first;
+      w[h] = ((int64_t)t->e * a.R + f) * pitch + 4 * step;
+      left[h] = a.R - f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) xs[i] = i == 0 || words ? t->row[first + 2 * i] : -1;
+    if (a.by_token) row_places(a, *t, row0, places);
+    tiles.done();
+    for (int kb = 0; kb < kbs; ++kb, ++s) {
+      const int slot = s % kStages, have = pitch - 16 * kb - 4 * step;
+      uint4 v[3];
+      if (!words) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v[h] = load_scales(a.wscale[h], w[h] + 16 * kb, left[h] > 0 ? have : 0,
+                             (int64_t)a.E * a.R * pitch);
+        v[2] = load_scales(a.xscale, (int64_t)xs[0] * pitch + 16 * kb, xs[0] >= 0 ? have : 0,
+                           (int64_t)a.x_rows * pitch);
+      }
+      if (s >= kStages && !wait_all(S, &S.empty[slot], (s / kStages - 1) & 1)) {
+        tiles.ok = false;
+        break;
+      }
+      if (a.by_token) copy_rows(a, S.codes[slot] + 2 * kOperand, row0, kb, places);
       uint8_t *dst = S.scales[slot] + line * 16 + j * 4;
+      if (words) {
+        auto copy = [&](uint8_t *to, const uint8_t *p, bool there) {
+          copy_async<4>(smem_addr(to), there ? p : a.wscale[0], there);
+        };
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          copy_word<kWords>(dst + step * kWeightPitch + h * kHalfPitch + i * 32,
-                            w[h] + (int64_t)(2 * i) * pitch + 16 * kb, a.wscale[0],
-                            2 * i < left[h] ? have : 0);
-      if (32 * j < rows) {
+          for (int i = 0; i < 4; ++i)
+            copy(dst + step * kWeightPitch + h * kHalfPitch + i * 32,
+                 a.wscale[h] + w[h] + (int64_t)(2 * i) * pitch + 16 * kb,
+                 2 * i < left[h] && have > 0);
+        if (32 * j < rows) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          copy_word<kWords>(dst + 4 * kWeightPitch + step * kRowPitch + i * 32,
-                            a.xscale + (int64_t)xs[i] * pitch + 4 * step + 16 * kb, a.wscale[0],
-                            xs[i] >= 0 ? have : 0);
+          for (int i = 0; i < 4; ++i)
+            copy(dst + 4 * kWeightPitch + step * kRowPitch + i * 32,
+                 a.xscale + (int64_t)xs[i] * pitch + 4 * step + 16 * kb, xs[i] >= 0 && have > 0);
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 3; ++h) {
+          uint8_t *to = dst + (h < 2 ? h * kHalfPitch : 4 * kWeightPitch);
+          const int next = h < 2 ? kWeightPitch : kRowPitch;
+          *reinterpret_cast<uint32_t *>(to) = v[h].x;
+          *reinterpret_cast<uint32_t *>(to + next) = v[h].y;
+          *reinterpret_cast<uint32_t *>(to + 2 * next) = v[h].z;
+          *reinterpret_cast<uint32_t *>(to + 3 * next) = v[h].w;
+        }
       }
       // the copies' own arrival, and this thread's for what it stored itself
       copies_arrive(&S.full[slot]);
-      if constexpr (!kWords) mbar_arrive(&S.full[slot]);
+      mbar_arrive(&S.full[slot]);
     }
     if (!tiles.ok) break;
   }
@@ -515,44 +711,59 @@ __device__ __forceinline__ void store_one(void *out, int64_t at, float v) {
     static_cast<float *>(out)[at] = v;
 }
 
-__device__ __forceinline__ void st_global_32(void *p, const uint32_t *w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
+// A lane's 32 neighbouring outputs of its row (in floats) to the warp's staging
+// rows of 128 bytes, `half` saying which half of a row of 16-bit ones; piece c
+// of row r goes to c ^ (r % 8), so that neither side of the exchange has bank
+// conflicts.  (Straight to global memory, a warp's store is 32 rows of 32 bytes:
+// that took the stores' pipe 125 clocks and held up every other copy; down of
+// 8192 rows 390 us.)
+template <typename T>
+__device__ __forceinline__ void stage_outputs(uint8_t *rows, int lane, int half,
+                                              const uint32_t (&v)[32]) {
+  constexpr int ES = sizeof(typename T::bits), PIECES = 32 * ES / 16;
+#pragma unroll
+  for (int c = 0; c < PIECES; ++c) {
+    uint4 q;
+    if constexpr (ES == 2) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = T::down2(__uint_as_float(v[8 * c + 2 * j]), __uint_as_float(v[8 * c + 2 * j + 1]));
+      q = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      q = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    }
+    *reinterpret_cast<uint4 *>(rows + lane * 128 +
+                               (((half * PIECES + c) ^ (lane & 7)) << 4)) = q;
+  }
 }
-
-// N neighbouring features of a row, in floats, from feature f on: whole sectors
-// of 32 bytes or pieces of 16 where rows allow them (`align`).
-template <typename T, int N>
-__device__ __forceinline__ void store_features(const ProductArgs &a, int64_t p, int f,
-                                               const uint32_t (&v)[N]) {
+// The staged rows (those of `real`) to positions p.. of the output from feature
+// f on: whole lines of 128 bytes where rows allow 16-byte pieces.
+template <typename T>
+__device__ __forceinline__ void store_staged(const ProductArgs &a, const uint8_t *rows, int lane,
+                                             uint32_t real, int p, int f) {
   using TB = typename T::bits;
-  constexpr int PER = 32 / (int)sizeof(TB);   // elements of a sector
-  TB *dst = static_cast<TB *>(a.out) + p * a.R + f;
+  constexpr int ES = sizeof(TB), N = 128 / ES, PER = 16 / ES;
+  __syncwarp();
   if (a.align >= 16) {
+    const int c = lane & 7, first = f + c * PER;
+    TB *dst = static_cast<TB *>(a.out) + (int64_t)p * a.R + first;
 #pragma unroll
-    for (int i = 0; i < N; i += PER) {
-      uint32_t w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if constexpr (sizeof(TB) == 2)
-          w[j] = T::down2(__uint_as_float(v[i + 2 * j]), __uint_as_float(v[i + 2 * j + 1]));
-        else
-          w[j] = v[i + j];
-      }
-      if (a.align == 32) {
-        if (f + i < a.R) st_global_32(dst + i, w);
-      } else {
-        if (f + i < a.R) *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (f + i + PER / 2 < a.R)
-          *reinterpret_cast<uint4 *>(dst + i + PER / 2) = make_uint4(w[4], w[5], w[6], w[7]);
-      }
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      const uint4 q = *reinterpret_cast<const uint4 *>(rows + r * 128 + ((c ^ (r & 7)) << 4));
+      if ((real >> r & 1) && first < a.R)
+        *reinterpret_cast<uint4 *>(dst + (int64_t)r * a.R) = q;
     }
   } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (f + i < a.R) store_one<T>(a.out, p * a.R + f + i, __uint_as_float(v[i]));
+    for (int r = 0; r < 32; ++r) {
+      if (!(real >> r & 1)) continue;
+      for (int e = lane; e < N && f + e < a.R; e += 32)
+        static_cast<TB *>(a.out)[(int64_t)(p + r) * a.R + f + e] = *reinterpret_cast<const TB *>(
+            rows + r * 128 + (((e / PER) ^ (r & 7)) << 4) + e % PER * ES);
+    }
   }
+  __syncwarp();
 }
 
 template <typename T, bool kPair>
@@ -602,7 +813,7 @@ __device__ void epilogue(const ProductArgs &a, Smem &S, uint32_t tmem) {
     }
     // lanes are rows, columns features: 128 for each group (64 of gate and of up)
     const int i = q * 32 + lane;
-    const bool real = t->row[i] >= 0;
+    const uint32_t real = __ballot_sync(kFull, t->row[i] >= 0);
     const float xg = t->xg[i];
     tiles.done();
     uint32_t v[4][32];
@@ -617,26 +828,30 @@ __device__ void epilogue(const ProductArgs &a, Smem &S, uint32_t tmem) {
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.acc_empty);
-    if (!real) continue;
+    if (!real) continue;   // none of the warp's rows
+    uint8_t *staged = S.staged[warp - kEpi0];
+    constexpr int H = sizeof(typename T::bits) == 2 ? 2 : 1;   // parts of 32 in 128 bytes
 #pragma unroll
     for (int h = 0; h < (kPair ? 2 : 4); ++h) {
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
         const float y = __uint_as_float(v[h][c]) * xg * g0;
         if constexpr (kPair)
-          v[h][c] = __float_as_uint(
-              silu_times(y, __uint_as_float(v[2 + h][c]) * xg * g1));
+          v[h][c] = __float_as_uint(silu_times(y, __uint_as_float(v[2 + h][c]) * xg * g1));
         else
           v[h][c] = __float_as_uint(y);
       }
-      store_features<T>(a, p0 + i, (kPair ? m * 128 + group * 64 : m * 256 + group * 128) + h * 32,
-                        v[h]);
+      stage_outputs<T>(staged, lane, h % H, v[h]);
+      if (h % H == H - 1)
+        store_staged<T>(a, staged, lane, real, p0 + q * 32,
+                        (kPair ? m * 128 + group * 64 : m * 256 + group * 128) +
+                            (h - h % H) * 32);
     }
   }
   if (!tiles.ok && lane == 0) fail(S, a);
 }
 
-template <typename T, bool kPair, bool kWords>
+template <typename T, bool kPair, bool kTmaScales>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_nvfp4_kernel(const __grid_constant__ ProductArgs a,
                          const __grid_constant__ ProductMaps maps) {
@@ -645,13 +860,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      // the TMA copies, and every thread of the copying warps (twice: copier)
-      mbar_init(&S.full[i], 1 + 128 * (kWords ? 1 : 2));
+      // the TMA copies; scales by TMA: each warp that turns them, and each thread
+      // that copies tokens' rows; else every copying thread, twice (copier)
+      mbar_init(&S.full[i], kTmaScales ? 1 + 4 + (a.by_token ? 128 : 0) : 1 + 256);
       mbar_init(&S.empty[i], 1);
+      mbar_init(&S.raw_full[i], 1);
+      mbar_init(&S.raw_empty[i], 4);
     }
     for (int i = 0; i < kInfos; ++i) {
       mbar_init(&S.info_full[i], 1);
-      mbar_init(&S.info_empty[i], 2 + 4 + kEpiWarps);
+      mbar_init(&S.info_empty[i], 2 + kTmaScales + 4 + kEpiWarps);
     }
     mbar_init(&S.acc_full, 1);
     mbar_init(&S.acc_empty, kEpiWarps);
@@ -666,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (warp == 0 && lane < 3) prefetch_tensormap(lane == 2 ? &maps.x : &maps.w[lane]);
+  if (warp == 0 && lane < (kPair ? 2 : 1)) prefetch_tensormap(&maps.w[lane]);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -712,7 +930,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     epilogue<T, kPair>(a, S, tmem);
   } else if (warp >= kCopyWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
-    copier<kPair, kWords>(a, S);
+    if constexpr (kTmaScales)
+      turner<kPair>(a, S);
+    else
+      copier<kPair>(a, S);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == 0)
@@ -721,6 +942,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_issuer<kPair>(a, S, tmem);
     else if (warp == 2)
       scheduler(a, S, total);
+    else if (kTmaScales)
+      scale_producer<kPair>(a, maps, S);
   }
 
   tc_fence_before();
@@ -785,6 +1008,7 @@ int grouped(const moe_proj *w0, const moe_proj *w1, int E, int R, int K, const u
   a.top_k = top_k;
   a.n = M * top_k;
   a.num_rows = num_rows;
+  a.x_rows = by_token ? M : num_rows;
   a.feature_tiles = w1 ? (R + 127) / 128 : (R + 255) / 256;
   a.offsets = offsets;
   a.sti = sti;
@@ -796,18 +1020,32 @@ int grouped(const moe_proj *w0, const moe_proj *w1, int E, int R, int K, const u
   a.xscale = scale;
   a.xglobal = global;
   a.out = out;
-  const uint64_t v = (uint64_t)(uintptr_t)out | (uint64_t)R * eb | 32;
+  const uint64_t v = (uint64_t)(uintptr_t)out | (uint64_t)R * eb | 16;
   a.align = (int)(v & (~v + 1));
   a.err = err;
   ProductMaps maps;
   memset(&maps, 0, sizeof(maps));
   const cuuint64_t pitch[1] = {(cuuint64_t)K / 2};
   const cuuint64_t wd[2] = {(cuuint64_t)K / 2, (cuuint64_t)E * R};
-  const cuuint64_t xd[2] = {(cuuint64_t)K / 2, (cuuint64_t)(by_token ? M : num_rows)};
-  const cuuint32_t wbox[2] = {128, 128}, xbox[2] = {128, 32};
-  for (int j = 0; j < 2; ++j)
+  const cuuint64_t xd[2] = {(cuuint64_t)K / 2, (cuuint64_t)a.x_rows};
+  const cuuint32_t half = w1 ? 128 : 256;   // weight rows of a copy
+  const cuuint32_t wbox[2] = {128, half}, xbox[2][2] = {{128, 32}, {128, 128}};
+  const cuuint64_t spitch[1] = {(cuuint64_t)K / 16};
+  const cuuint64_t wsd[2] = {(cuuint64_t)K / 16, wd[1]}, xsd[2] = {(cuuint64_t)K / 16, xd[1]};
+  const cuuint32_t wsbox[2] = {16, half}, xsbox[2] = {16, 128};
+  const bool tma_scales = K % 256 == 0;
+  for (int j = 0; j < (w1 ? 2 : 1); ++j) {
     if (const int st = encode_u8_sw128(&maps.w[j], w[j]->codes, 2, wd, pitch, wbox)) return st;
-  if (const int st = encode_u8_sw128(&maps.x, codes, 2, xd, pitch, xbox)) return st;
+    if (tma_scales)
+      if (const int st = encode_u8_plain(&maps.ws[j], w[j]->scale, 2, wsd, spitch, wsbox))
+        return st;
+  }
+  if (!by_token) {   // tokens' rows are copied by threads
+    for (int j = 0; j < 2; ++j)
+      if (const int st = encode_u8_sw128(&maps.x[j], codes, 2, xd, pitch, xbox[j])) return st;
+    if (tma_scales)
+      if (const int st = encode_u8_plain(&maps.xs, scale, 2, xsd, spitch, xsbox)) return st;
+  }
 
   // an upper bound of the tiles: experts have at most a tile more than whole ones
   const int64_t slots = a.n < E ? a.n : E;
@@ -821,7 +1059,7 @@ int grouped(const moe_proj *w0, const moe_proj *w1, int E, int R, int K, const u
       if (const int st = ensure_registers((const void *)kernel)) return st;
       return launch_pdl(kernel, grid, dim3(kThreads), kSmemBytes, stream, a, maps);
     };
-    if (K % 64 == 0) return launch(grouped_nvfp4_kernel<T, P, true>);
+    if (tma_scales) return launch(grouped_nvfp4_kernel<T, P, true>);
     return launch(grouped_nvfp4_kernel<T, P, false>);
   };
   auto typed = [&](auto pair) {
