@@ -863,12 +863,13 @@ def moe_decode_block(layer: LayerDesc, x: torch.Tensor, residual: Optional[torch
 # four-bit rows, and the products of four-bit rows and weights
 # --------------------------------------------------------------------------
 
-_BYTES = (torch.uint8, torch.float8_e4m3fn)
+_U8, _E4M3, _F32 = torch.uint8, torch.float8_e4m3fn, torch.float32
 
 
 def _bytes_at(name: str, t: torch.Tensor, shape: tuple) -> int:
     """The address of a dense buffer of bytes (scales: E4M3 values too)."""
-    if t.dtype not in _BYTES or t.shape != shape or not t.is_contiguous():
+    dtype = t.dtype
+    if (dtype is not _U8 and dtype is not _E4M3) or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: want a contiguous uint8 tensor of shape {shape}, "
                          f"got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
@@ -881,15 +882,16 @@ def _packed(name: str, q) -> tuple:
         return q["codes"], q["scale"], q["global_scale"]
     if len(q) != 3:
         raise ValueError(f"{name}: want codes, scale and global_scale")
-    return tuple(q)
+    return q
 
 
-def _packed_at(name: str, q, lead: tuple, cols: int) -> tuple:
-    """Their addresses, for codes of [*lead, cols / 2] bytes."""
+def _packed_at(name: str, q: tuple, codes_shape: tuple, scale_shape: tuple) -> tuple:
+    """Their addresses."""
     codes, scale, glob = q
-    return (_bytes_at(f"{name} codes", codes, (*lead, cols // 2)),
-            _bytes_at(f"{name} scale", scale, (*lead, cols // 16)),
-            _at(f"{name} global_scale", glob, torch.float32, (lead[0],)))
+    if codes.dtype is not _U8:
+        raise ValueError(f"{name} codes: want uint8, got {codes.dtype}")
+    return (_bytes_at(name, codes, codes_shape), _bytes_at(name, scale, scale_shape),
+            _at(name, glob, _F32, codes_shape[:1]))
 
 
 def quantize_nvfp4_workspace_bytes(groups: int, rows: int, cols: int) -> int:
@@ -899,17 +901,16 @@ def quantize_nvfp4_workspace_bytes(groups: int, rows: int, cols: int) -> int:
     return nbytes
 
 
-def _quantized(name: str, x: torch.Tensor) -> tuple:
+def _quantized(name: str, dtype: torch.dtype, shape: tuple) -> tuple:
     """(shape, type) of an output of moe_quantize_nvfp4 on x."""
-    *lead, cols = x.shape
     if name == "codes":
-        return (*lead, cols // 2), torch.uint8
+        return (*shape[:-1], shape[-1] // 2), _U8
     if name == "scale":
-        return (*lead, cols // 16), torch.uint8
+        return (*shape[:-1], shape[-1] // 16), _U8
     if name == "global_scale":
-        return (lead[0],), torch.float32
+        return shape[:1], _F32
     if name == "values":
-        return tuple(x.shape), x.dtype
+        return shape, dtype
     raise ValueError(f"no output {name!r}: want codes, scale, global_scale or values")
 
 
@@ -917,7 +918,8 @@ def alloc_quantize_nvfp4_outputs(x: torch.Tensor,
                                  want: Sequence[str] = ("codes", "scale", "global_scale"),
                                  stream=None) -> dict:
     """Buffers for moe_quantize_nvfp4 of x."""
-    return {name: _empty(*_quantized(name, x), x.device, stream) for name in want}
+    shape, dtype, device = tuple(x.shape), x.dtype, x.device
+    return {name: _empty(*_quantized(name, dtype, shape), device, stream) for name in want}
 
 
 def moe_quantize_nvfp4(x: torch.Tensor, want: Sequence[str] = ("codes", "scale", "global_scale"),
@@ -932,45 +934,45 @@ def moe_quantize_nvfp4(x: torch.Tensor, want: Sequence[str] = ("codes", "scale",
     gradients straight through the rounding).  With ``tables``, x's rows are in
     expert order and the padding rows are skipped.  Writes the buffers of
     ``out``, or new ones for the outputs in ``want``, and returns them by name."""
-    if x.dim() not in (2, 3):
-        raise ValueError(f"x: want [M, H] or [E, rows, cols], got {tuple(x.shape)}")
-    dtype, kind, shape = x.dtype, _kind("x", x, _FLOAT), x.shape
-    groups, cols = shape[0], shape[-1]
-    rows = shape[1] if len(shape) == 3 else 1
-    if len(shape) == 3:
+    dtype, kind, shape = x.dtype, _kind("x", x, _FLOAT), tuple(x.shape)
+    if len(shape) == 2:
+        groups, cols = shape
+        rows, stride = 1, _row_stride("x", x, dtype, shape)
+    elif len(shape) == 3:
+        groups, rows, cols = shape
         s0, s1, s2 = x.stride()
         stride = s1 if rows > 1 else s0 if groups > 1 else cols
         if (s2 != 1 and cols > 1) or (groups > 1 and rows > 1 and s0 != rows * s1):
             raise ValueError(f"x: want evenly spaced dense rows, got strides {x.stride()}")
     else:
-        stride = _row_stride("x", x, dtype, (groups, cols))
-    s_at, n = None, 0
+        raise ValueError(f"x: want [M, H] or [E, rows, cols], got {shape}")
+    sti = s_at = g_at = None
+    n = 0
     if tables is not None:
         sti = tables["sorted_token_ids"]
-        if len(shape) == 3 or _num_rows(tables) != groups:
-            raise ValueError(f"x: want the tables' {_num_rows(tables)} rows, got {tuple(shape)}")
+        if rows != 1 or len(shape) == 3 or _num_rows(tables) != groups:
+            raise ValueError(f"x: want the tables' {_num_rows(tables)} rows, got {shape}")
         s_at, n = _table("sorted_token_ids", sti, groups), tables["token_to_perm"].numel()
-    g_at = None
     if global_scale is not None:
-        g_at = _at("global_scale", global_scale, torch.float32, (groups,))
+        g_at = _at("global_scale", global_scale, _F32, (groups,))
     at = {}
     if out is not None:
         for name, t in out.items():
-            oshape, otype = _quantized(name, x)
-            at[name] = _bytes_at(name, t, oshape) if otype is torch.uint8 else \
-                _at(name, t, otype, oshape)
-    dev = _on_device(x, global_scale, workspace, *(() if tables is None else (sti,)),
-                     *(() if out is None else out.values()))
-    if out is None:
-        out = {}
+            oshape, otype = _quantized(name, dtype, shape)
+            at[name] = _bytes_at(name, t, oshape) if otype is _U8 else _at(name, t, otype, oshape)
+        dev = _on_device(x, global_scale, workspace, sti, *out.values())
+    else:
+        dev, device, out = _on_device(x, global_scale, workspace, sti), x.device, {}
         for name in want:
-            t = out[name] = _empty(*_quantized(name, x), x.device, stream)
+            oshape, otype = _quantized(name, dtype, shape)
+            t = out[name] = torch.empty(oshape, dtype=otype, device=device) if stream is None \
+                else _empty(oshape, otype, device, stream)
             at[name] = t.data_ptr()
     nbytes, ws_at = 0, None
     if rows > 1 and g_at is None:
         if workspace is None:
-            workspace = _empty((quantize_nvfp4_workspace_bytes(groups, rows, cols),), torch.uint8,
-                               x.device, stream)
+            workspace = _empty((quantize_nvfp4_workspace_bytes(groups, rows, cols),), _U8, x.device,
+                               stream)
         elif not workspace.is_contiguous():
             raise ValueError("workspace: want a contiguous tensor")
         ws_at, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -986,10 +988,11 @@ def moe_dequantize_nvfp4(codes: torch.Tensor, scale: torch.Tensor, global_scale:
                          stream=None) -> torch.Tensor:
     """The values of NVFP4 codes [M, H / 2] or [E, rows, cols / 2], of ``dtype``
     (or out's type): code * (scale * global_scale), rounded once."""
-    if codes.dim() not in (2, 3):
-        raise ValueError(f"codes: want [M, H / 2] or [E, rows, cols / 2], got {tuple(codes.shape)}")
     lead, cols = tuple(codes.shape[:-1]), 2 * codes.shape[-1]
-    c_at, s_at, g_at = _packed_at("rows", (codes, scale, global_scale), lead, cols)
+    if not 1 <= len(lead) <= 2:
+        raise ValueError(f"codes: want [M, H / 2] or [E, rows, cols / 2], got {tuple(codes.shape)}")
+    c_at, s_at, g_at = _packed_at("rows", (codes, scale, global_scale), (*lead, cols // 2),
+                                  (*lead, cols // 16))
     if out is not None:
         dtype = out.dtype
     kind = _FLOAT.get(dtype)
@@ -1009,19 +1012,20 @@ def moe_dequantize_nvfp4(codes: torch.Tensor, scale: torch.Tensor, global_scale:
 def _grouped_nvfp4(fn: str, sets: tuple, rows, tables: dict, top_k: int, M: Optional[int],
                    out: Optional[torch.Tensor], out_dtype: Optional[torch.dtype], err_word,
                    stream) -> torch.Tensor:
-    sets = tuple(_packed("weight", w) for w in sets)
-    if sets[0][0].dim() != 3:
-        raise ValueError(f"weight codes: want [E, rows, cols / 2], got {tuple(sets[0][0].shape)}")
-    E, R, C = sets[0][0].shape
+    sets = [_packed("weight", w) for w in sets]
+    shape = tuple(sets[0][0].shape)
+    if len(shape) != 3:
+        raise ValueError(f"weight codes: want [E, rows, cols / 2], got {shape}")
+    E, R, C = shape
     C *= 2
-    projs = []
-    for w in sets:
-        projs.append(_Proj(*_packed_at("weight", w, (E, R), C)))
-    codes, scale, glob = _packed("rows", rows)
+    w_shape = (E, R, C // 16)
+    projs = [_Proj(*_packed_at("weight", w, shape, w_shape)) for w in sets]
+    codes, scale, glob = x = _packed("rows", rows)
     by_token, n_rows = M is None, _num_rows(tables)
     if by_token:
         M = codes.shape[0]
-    x_at = _packed_at("rows", (codes, scale, glob), (M if by_token else n_rows,), C)
+    n = M if by_token else n_rows
+    x_at = _packed_at("rows", x, (n, C // 2), (n, C // 16))
     offs, sti = tables["expert_offsets"], tables["sorted_token_ids"]
     f_at, s_at = _table("expert_offsets", offs, E + 1), _table("sorted_token_ids", sti, n_rows)
     e_at = _err(err_word)
@@ -1030,13 +1034,13 @@ def _grouped_nvfp4(fn: str, sets: tuple, rows, tables: dict, top_k: int, M: Opti
     if okind is None:
         raise ValueError(f"out: unsupported type {otype}")
     o_at = None if out is None else _at("out", out, otype, (n_rows, R))
-    dev = _on_device(codes, scale, glob, *(t for w in sets for t in w), offs, sti, out, err_word)
+    dev = _on_device(codes, scale, glob, *sets[0], *(sets[1] if len(sets) > 1 else ()), offs, sti,
+                     out, err_word)
     if o_at is None:
         out = _empty((n_rows, R), otype, codes.device, stream)
         o_at = out.data_ptr()
-    _check(fn, getattr(load(), fn)(
-        *(ctypes.byref(p) for p in projs), E, R, C, *x_at, int(by_token), M, top_k, f_at, s_at,
-        n_rows, okind, o_at, e_at, _handle(stream, dev)))
+    _check(fn, getattr(load(), fn)(*map(ctypes.byref, projs), E, R, C, *x_at, by_token, M, top_k,
+                                   f_at, s_at, n_rows, okind, o_at, e_at, _handle(stream, dev)))
     return out
 
 

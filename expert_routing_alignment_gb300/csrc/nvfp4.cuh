@@ -1,5 +1,6 @@
 // nvfp4.cuh -- blocks of 16 elements in NVFP4 (E2M1 codes under an E4M3 scale
-// and an fp32 global scale): encoding and decoding.
+// and an fp32 global scale): a thread encodes a whole block, and decodes pieces of
+// 16 bytes, a block being two of a 16-bit type or four of fp32.
 #pragma once
 
 #include "rows.cuh"
@@ -13,6 +14,12 @@ constexpr float kGlobalDiv = kE2m1Max * kE4m3Most;   // a group's maximum over i
 // the residuals of the quotients (2^-49 of an element of a step's size) among
 // the numbers that fp32 holds exactly.
 constexpr float kGlobalMin = 0x1p-80f;
+
+// Pieces of a block, and the type of a piece's packed codes.
+template <typename T>
+constexpr int kPieces16 = kBlock16 / kPer16<T>;
+template <int N> struct PackedCodes { using type = uint32_t; };
+template <> struct PackedCodes<4> { using type = uint16_t; };
 
 // Eight floats to E2M1, ties to even, saturating at 6; the first in the low
 // nibble.
@@ -30,111 +37,149 @@ __device__ __forceinline__ uint32_t to_e2m1x8(const f32x2 *f) {
   return r;
 }
 
-// Eight codes to floats (exact).
-__device__ __forceinline__ void from_e2m1x8(uint32_t v, f32x2 *f) {
+// The values of N codes under the step t, code * t.
+template <int N>
+__device__ __forceinline__ void code_values(uint32_t codes, float t, f32x2 *f) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 p = f16x2_to_float2(e2m1x2_to_f16x2((v >> (8 * i)) & 0xFFu));
-    f[i] = pair(p.x, p.y);
+  for (int i = 0; i < N / 2; ++i) {
+    const float2 p = f16x2_to_float2(e2m1x2_to_f16x2((codes >> (8 * i)) & 0xFFu));
+    f[i] = mul2(pair(p.x, p.y), pair(t, t));
   }
 }
 
-// The largest magnitude of a block, NaN if it has one.
-__device__ __forceinline__ float block_max(const f32x2 (&f)[8]) {
-  float m = 0.f;
+// A block as it is stored.  How it is moved: by 32-byte sectors (kSectors), 16-byte
+// pieces (kWhole) or elements (kElems).
+enum { kSectors = 32 };
+template <typename T>
+using RawBlock = Raw<T, kBlock16>;
+template <typename T, int A>
+__device__ __forceinline__ RawBlock<T> block_load(const typename T::bits *row, int b) {
+  RawBlock<T> r;
+  const typename T::bits *p = row + (size_t)b * kBlock16;
+  if constexpr (A == kSectors) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 p = unpair(f[i]);
-    m = max_abs_nan(m, p.x, p.y);
+    for (int i = 0; i < RawBlock<T>::kWords; i += 8)
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(r.w[i]), "=r"(r.w[i + 1]), "=r"(r.w[i + 2]), "=r"(r.w[i + 3]),
+                     "=r"(r.w[i + 4]), "=r"(r.w[i + 5]), "=r"(r.w[i + 6]), "=r"(r.w[i + 7])
+                   : "l"(reinterpret_cast<const uint32_t *>(p) + i));
+  } else if constexpr (A == kWhole) {
+    r = raw_load_aligned<T, kBlock16>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < RawBlock<T>::kWords; ++i) {
+      if constexpr (sizeof(typename T::bits) == 4)
+        r.w[i] = p[i];
+      else
+        r.w[i] = (uint32_t)p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
+    }
+  }
+  return r;
+}
+template <typename T, int A>
+__device__ __forceinline__ void block_store(typename T::bits *row, int b, const RawBlock<T> &r) {
+  typename T::bits *p = row + (size_t)b * kBlock16;
+  if constexpr (A == kSectors) {
+#pragma unroll
+    for (int i = 0; i < RawBlock<T>::kWords; i += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                       reinterpret_cast<uint32_t *>(p) + i),
+                   "r"(r.w[i]), "r"(r.w[i + 1]), "r"(r.w[i + 2]), "r"(r.w[i + 3]), "r"(r.w[i + 4]),
+                   "r"(r.w[i + 5]), "r"(r.w[i + 6]), "r"(r.w[i + 7])
+                   : "memory");
+  } else if constexpr (A == kWhole) {
+#pragma unroll
+    for (int i = 0; i < RawBlock<T>::kWords; i += 4)
+      *reinterpret_cast<uint4 *>(reinterpret_cast<uint32_t *>(p) + i) =
+          make_uint4(r.w[i], r.w[i + 1], r.w[i + 2], r.w[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < RawBlock<T>::kWords; ++i) {
+      if constexpr (sizeof(typename T::bits) == 4) {
+        p[i] = r.w[i];
+      } else {
+        p[2 * i] = (uint16_t)r.w[i];
+        p[2 * i + 1] = (uint16_t)(r.w[i] >> 16);
+      }
+    }
+  }
+}
+
+// The largest magnitude of a block; NaN if it has one.
+template <typename T>
+__device__ __forceinline__ float block_max(const RawBlock<T> &r) {
+  float m = 0.f;
+  if constexpr (sizeof(typename T::bits) == 2) {
+    uint32_t w = r.w[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) w = T::max2(w, r.w[i] & 0x7FFF7FFFu);
+    const float2 p = T::up2(w);
+    m = max_nan(p.x, p.y);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; i += 2)
+      m = max_abs_nan(m, __uint_as_float(r.w[i]), __uint_as_float(r.w[i + 1]));
   }
   return m;
 }
 // What a block's maximum adds to its group's: blocks with a NaN or an infinity
 // have no part in it.
-__device__ __forceinline__ float finite_max(float m) { return m < __int_as_float(0x7F800000) ? m : 0.f; }
-
+__device__ __forceinline__ float finite_max(float m) {
+  return m < __int_as_float(0x7F800000) ? m : 0.f;
+}
 // The global scale of a group whose largest magnitude is m.
 __device__ __forceinline__ float global_of(float m) { return fmaxf(m / kGlobalDiv, kGlobalMin); }
 
-// A block's scale byte from its maximum m and the global scale g:
+// A quotient a / b from y = 1 / b to a unit or two of its last place: a y,
+// corrected by its residual a - q b (one fma, exact) times y, is the float next
+// to a / b, so that ties of the roundings that follow are where the division
+// puts them (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990).
+__device__ __forceinline__ f32x2 quotient2(f32x2 a, f32x2 minus_b, f32x2 y) {
+  const f32x2 q = mul2(a, y);
+  return fma2(fma2(q, minus_b, a), y, q);
+}
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// A group's scale and what its blocks' scales divide by.
+struct GlobalScale {
+  float g, six, inv;
+  __device__ __forceinline__ explicit GlobalScale(float v)
+      : g(v), six(kE2m1Max * v), inv(1.f / (kE2m1Max * v)) {}
+};
+
+// A block's scale byte from its maximum m:
 //   s = e4m3(min(m / (6 g), 448)), NaN for a block with a NaN or an infinity.
-__device__ __forceinline__ uint32_t block_scale(float m, float g) {
-  float r = m / (kE2m1Max * g);
+// Quotients over 2^60 (a given scale far below the values) go without the
+// residual, which could leave fp32's range.
+__device__ __forceinline__ uint32_t block_scale(float m, const GlobalScale &g) {
+  const float q = m * g.inv;
+  float r = q < 0x1p60f ? fmaf(fmaf(-q, g.six, m), g.inv, q) : q;
   if (!(m < __int_as_float(0x7F800000))) r = __int_as_float(0x7FFFFFFF);
   return to_e4m3x2(r, 0.f) & 0xFFu;
 }
 
-// A block's codes, e2m1(x / t) with t the block's step s * g in fp32, and 0
-// throughout where s is 0 or NaN.  The quotient is x times y = 1 / t rounded,
-// corrected by its residual x - q t (one fma) times y: the nearest float to
-// x / t, so that ties of the rounding to a code are where the division puts
-// them (Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990).  One division a block instead of one an
-// element.  A quotient over 2^60 (a given global scale far below the values)
-// goes without the residual, which could leave fp32's range.
-__device__ __forceinline__ uint2 block_codes(f32x2 (&f)[8], float s, float t, float m) {
-  if (!(s > 0.f)) return make_uint2(0u, 0u);
-  const float y = 1.f / t;
+// The codes of a block with the step t (its scale s times the global one) and the
+// maximum m: e2m1(x / t), and 0 throughout where s is 0 or NaN.
+template <typename T>
+__device__ __forceinline__ uint2 block_codes(const RawBlock<T> &r, float s, float t, float m) {
+  f32x2 f[8];
+  raw_up<T, kBlock16>(r, f);
+  const float y = reciprocal(t);
   const f32x2 yy = pair(y, y), mt = pair(-t, -t);
   if (m * y < 0x1p60f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const f32x2 q = mul2(f[i], yy);
-      f[i] = fma2(fma2(q, mt, f[i]), yy, q);
-    }
+    for (int i = 0; i < 8; ++i) f[i] = quotient2(f[i], mt, yy);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = mul2(f[i], yy);
   }
-  return make_uint2(to_e2m1x8(f), to_e2m1x8(f + 4));
-}
-
-// The values of a block's codes, code * t.
-__device__ __forceinline__ void block_values(uint2 codes, float t, f32x2 (&f)[8]) {
-  from_e2m1x8(codes.x, f);
-  from_e2m1x8(codes.y, f + 4);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = mul2(f[i], pair(t, t));
-}
-
-// Block b of a row of H elements (H a multiple of 16) as stored: 16-byte
-// pieces (kWhole) or elements (kElems).
-template <typename T>
-constexpr int kPieces16 = kBlock16 / kPer16<T>;
-template <typename T>
-struct RawBlock {
-  Raw<T, kPer16<T>> p[kPieces16<T>];
-};
-template <typename T, int A>
-__device__ __forceinline__ RawBlock<T> block_load(const typename T::bits *row, int b, int H) {
-  RawBlock<T> r;
-#pragma unroll
-  for (int i = 0; i < kPieces16<T>; ++i)
-    r.p[i] = raw_load<T, kPer16<T>, A>(row, b * kPieces16<T> + i, H);
-  return r;
-}
-template <typename T>
-__device__ __forceinline__ void block_up(const RawBlock<T> &r, f32x2 (&f)[8]) {
-  constexpr int N = kPer16<T>;
-#pragma unroll
-  for (int i = 0; i < kPieces16<T>; ++i) {
-    f32x2 v[N / 2];
-    raw_up<T, N>(r.p[i], v);
-#pragma unroll
-    for (int e = 0; e < N / 2; ++e) f[i * N / 2 + e] = v[e];
-  }
-}
-template <typename T, int A>
-__device__ __forceinline__ void block_store(typename T::bits *row, int b, int H,
-                                            const f32x2 (&f)[8]) {
-  constexpr int N = kPer16<T>;
-#pragma unroll
-  for (int i = 0; i < kPieces16<T>; ++i) {
-    f32x2 v[N / 2];
-#pragma unroll
-    for (int e = 0; e < N / 2; ++e) v[e] = f[i * N / 2 + e];
-    raw_store<T, N, A>(row, b * kPieces16<T> + i, H, raw_down<T>(v));
-  }
+  const uint2 c = make_uint2(to_e2m1x8(f), to_e2m1x8(f + 4));
+  return s > 0.f ? c : make_uint2(0u, 0u);
 }
 
 }  // namespace moe

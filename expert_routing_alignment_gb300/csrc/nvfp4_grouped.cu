@@ -40,6 +40,7 @@
 //    the epilogue, which takes the accumulators into registers first, so that
 //    the next tile's MMAs run beside its arithmetic and stores.  The roles meet at mbarriers alone;
 //    every wait gives up after about two seconds with MOE_ERR_TIMEOUT.
+#include <atomic>
 #include <cstring>
 
 #include "nvfp4.cuh"
@@ -103,7 +104,6 @@ struct ProductMaps {
 struct TileInfo {
   int e, m, p0, rows;       // expert, feature tile, first position, rows up to the last real one
   int row[kTileRows];       // the row that each position reads, -1: none
-  float xg[kTileRows];      // its global scale
 };
 
 struct Smem {
@@ -119,6 +119,7 @@ struct Smem {
   uint32_t tmem;
   int warp_sum[kWarps];
   int tiles[MOE_MAX_EXPERTS + 1];   // row tiles ahead of each expert's
+  int begin[MOE_MAX_EXPERTS + 1];   // the runs' first positions
 };
 
 // ---------------------------------------------------------------------------
@@ -191,8 +192,6 @@ __device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x,
 // tiles
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ int clamp_to(int v, int hi) { return v < 0 ? 0 : v > hi ? hi : v; }
-
 __device__ __forceinline__ void fail(Smem &S, const ProductArgs &a) {
   *(volatile int *)&S.failed = 1;
   if (a.err) atomicOr(a.err, MOE_ERR_TIMEOUT);
@@ -217,7 +216,6 @@ __device__ void scheduler(const ProductArgs &a, Smem &S, int total) {
   uint32_t n = 0;
   for (int idx = blockIdx.x;; idx += gridDim.x) {
     int e = 0, m = 0, p0 = 0, rows = -1, r[4];
-    float xg[4];
     if (idx < total) {
       int hi = a.E - 1;   // e: the last expert whose tiles begin at or ahead of idx
       while (e < hi) {
@@ -229,8 +227,8 @@ __device__ void scheduler(const ProductArgs &a, Smem &S, int total) {
       }
       const int rt = S.tiles[e + 1] - S.tiles[e], at = idx - S.tiles[e] * mt;
       m = at / rt;
-      p0 = clamp_to(a.offsets[e], a.num_rows) + (at - m * rt) * kTileRows;
-      const int len = min(kTileRows, clamp_to(a.offsets[e + 1], a.num_rows) - p0);
+      p0 = S.begin[e] + (at - m * rt) * kTileRows;
+      const int len = min(kTileRows, S.begin[e + 1] - p0);
       rows = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -240,8 +238,6 @@ __device__ void scheduler(const ProductArgs &a, Smem &S, int total) {
         if (r[j] >= 0) rows = i + 1;
         if ((s < 0 || s > a.n) && a.err) atomicOr(a.err, MOE_ERR_BAD_POSITION);
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) xg[j] = r[j] >= 0 ? a.xglobal[r[j]] : 0.f;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) rows = max(rows, __shfl_xor_sync(kFull, rows, d));
       if (!rows) continue;
@@ -253,10 +249,7 @@ __device__ void scheduler(const ProductArgs &a, Smem &S, int total) {
     }
     TileInfo &t = S.info[slot];
     if (lane == 0) *reinterpret_cast<int4 *>(&t.e) = make_int4(e, m, p0, rows);
-    if (rows > 0) {
-      *reinterpret_cast<int4 *>(&t.row[4 * lane]) = make_int4(r[0], r[1], r[2], r[3]);
-      *reinterpret_cast<float4 *>(&t.xg[4 * lane]) = make_float4(xg[0], xg[1], xg[2], xg[3]);
-    }
+    if (rows > 0) *reinterpret_cast<int4 *>(&t.row[4 * lane]) = make_int4(r[0], r[1], r[2], r[3]);
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.info_full[slot]);
     if (rows < 0) return;
@@ -776,6 +769,10 @@ __device__ void epilogue(const ProductArgs &a, Smem &S, uint32_t tmem) {
     const int rows = t->rows, m = t->m, p0 = t->p0;
     const bool few = rows <= kFewRows;
     const float g0 = a.wglobal[0][t->e], g1 = a.wglobal[1][t->e];
+    // this lane's row (of few: of the group's columns), its global scale
+    const int i = few ? group * 16 + (lane & 15) : q * 32 + lane, x = t->row[i];
+    const float xg = x >= 0 ? a.xglobal[x] : 0.f;
+    const uint32_t real = __ballot_sync(kFull, x >= 0);
     if (!wait_all(S, &S.acc_full, tiles.n & 1)) {
       tiles.ok = false;
       break;
@@ -797,10 +794,10 @@ __device__ void epilogue(const ProductArgs &a, Smem &S, uint32_t tmem) {
       const int f1 = feature_of<kPair>(m, 1) + q * 32 + lane;
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        if (c0 + c >= rows || t->row[c0 + c] < 0) continue;
-        const float xg = t->xg[c0 + c];
+        const float xc = __shfl_sync(kFull, xg, c);
+        if (!(real >> c & 1)) continue;
         const int64_t at = (int64_t)(p0 + c0 + c) * a.R;
-        const float y0 = __uint_as_float(v0[c]) * xg * g0, y1 = __uint_as_float(v1[c]) * xg * g1;
+        const float y0 = __uint_as_float(v0[c]) * xc * g0, y1 = __uint_as_float(v1[c]) * xc * g1;
         if constexpr (kPair) {
           if (f0 < a.R) store_one<T>(a.out, at + f0, silu_times(y0, y1));
         } else {
@@ -812,9 +809,6 @@ __device__ void epilogue(const ProductArgs &a, Smem &S, uint32_t tmem) {
       continue;
     }
     // lanes are rows, columns features: 128 for each group (64 of gate and of up)
-    const int i = q * 32 + lane;
-    const uint32_t real = __ballot_sync(kFull, t->row[i] >= 0);
-    const float xg = t->xg[i];
     tiles.done();
     uint32_t v[4][32];
     if (q * 32 < rows) {
@@ -900,9 +894,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     run[i] = 0;
     if (e < a.E) {
       const int b = a.offsets[e], d = a.offsets[e + 1];
+      S.begin[e] = b;
+      if (e == a.E - 1) S.begin[a.E] = d;
       bad |= b < 0 || d < b || d > a.num_rows;
-      const int len = clamp_to(d, a.num_rows) - clamp_to(b, a.num_rows);
-      run[i] = len > 0 ? (len + kTileRows - 1) / kTileRows : 0;
+      run[i] = d > b && !bad ? (d - b + kTileRows - 1) / kTileRows : 0;
     }
   }
   // tables that are none: nothing is computed (their tiles could be any number)
@@ -962,16 +957,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;   // with its alignment
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
-// A warpgroup that asks for registers waits until the others have given up
-// theirs: a kernel that was built with fewer at launch must not run.
-int ensure_registers(const void *kernel) {
-  cudaFuncAttributes attr;
-  const cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
-  if (e != cudaSuccess) {
-    set_last_cuda_error(e);
-    return MOE_ECUDA;
+template <typename T, bool kPair, bool kTmaScales>
+int launch_grouped(const ProductArgs &a, const ProductMaps &maps, dim3 grid, void *stream) {
+  const auto kernel = grouped_nvfp4_kernel<T, kPair, kTmaScales>;
+  if (const int st = ensure_smem_limit((const void *)kernel, kSmemBytes)) return st;
+  // A warpgroup that asks for registers waits until the others have given up
+  // theirs: a kernel that was built with fewer at launch must not run.  (Looked
+  // up until known: a property of the program, the same on every device.)
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) != kLaunchRegs) {
+    cudaFuncAttributes attr;
+    const cudaError_t e = cudaFuncGetAttributes(&attr, (const void *)kernel);
+    if (e != cudaSuccess) {
+      set_last_cuda_error(e);
+      return MOE_ECUDA;
+    }
+    if (attr.numRegs != kLaunchRegs) return MOE_EUNSUPPORTED;
+    regs.store(attr.numRegs, std::memory_order_relaxed);
   }
-  return attr.numRegs == kLaunchRegs ? MOE_OK : MOE_EUNSUPPORTED;
+  return launch_pdl(kernel, grid, dim3(kThreads), kSmemBytes, stream, a, maps);
 }
 
 bool misaligned(const void *p, uintptr_t bytes) { return ((uintptr_t)p & (bytes - 1)) != 0; }
@@ -1054,13 +1058,8 @@ int grouped(const moe_proj *w0, const moe_proj *w1, int E, int R, int K, const u
   auto go = [&](auto t, auto pair) {
     using T = decltype(t);
     constexpr bool P = decltype(pair)::value;
-    auto launch = [&](auto kernel) {
-      if (const int st = ensure_smem_limit((const void *)kernel, kSmemBytes)) return st;
-      if (const int st = ensure_registers((const void *)kernel)) return st;
-      return launch_pdl(kernel, grid, dim3(kThreads), kSmemBytes, stream, a, maps);
-    };
-    if (tma_scales) return launch(grouped_nvfp4_kernel<T, P, true>);
-    return launch(grouped_nvfp4_kernel<T, P, false>);
+    return tma_scales ? launch_grouped<T, P, true>(a, maps, grid, stream)
+                      : launch_grouped<T, P, false>(a, maps, grid, stream);
   };
   auto typed = [&](auto pair) {
     switch (dtype) {

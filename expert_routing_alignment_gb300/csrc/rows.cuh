@@ -71,6 +71,12 @@ struct BF16 {
   static __device__ __forceinline__ float2 up2(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
   }
+  // the larger ones, NaN if there is one
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
 };
 struct F16 {
   using bits = uint16_t;
@@ -85,6 +91,11 @@ struct F16 {
     return r;
   }
   static __device__ __forceinline__ float2 up2(uint32_t v) { return f16x2_to_float2(v); }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
 };
 struct F32 {
   using bits = uint32_t;
