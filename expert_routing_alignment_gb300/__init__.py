@@ -965,8 +965,11 @@ def moe_quantize_nvfp4(x: torch.Tensor, want: Sequence[str] = ("codes", "scale",
         dev, device, out = _on_device(x, global_scale, workspace, sti), x.device, {}
         for name in want:
             oshape, otype = _quantized(name, dtype, shape)
-            t = out[name] = torch.empty(oshape, dtype=otype, device=device) if stream is None \
-                else _empty(oshape, otype, device, stream)
+            if stream is None:   # as _empty, without a call
+                t = torch.empty(oshape, dtype=otype, device=device)
+            else:
+                t = _empty(oshape, otype, device, stream)
+            out[name] = t
             at[name] = t.data_ptr()
     nbytes, ws_at = 0, None
     if rows > 1 and g_at is None:
