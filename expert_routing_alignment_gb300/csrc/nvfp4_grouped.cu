@@ -79,7 +79,8 @@ constexpr uint32_t kTileCols = 128, kScaleBase = 256, kScaleCols = 48, kRowScale
 
 struct ProductArgs {
   int E, R, K;               // experts, output features, input features
-  int by_token, top_k, n;    // n slots
+  int by_token, n;           // n slots
+  uint32_t per_k;            // 2^32 / top_k, rounded up (0: top_k 1): slots are below 2^20
   int num_rows;              // of the expert-order buffers
   int x_rows;                // of the rows' codes and scales
   int align;                 // of the output's rows, in bytes: 16 or less
@@ -100,10 +101,11 @@ struct ProductMaps {
   CUtensorMap w[2], x[2], ws[2], xs;
 };
 
-// A tile as every role reads it; rows < 0: no more tiles.
+// A tile as every role reads it: its place first, then its rows.
 struct TileInfo {
-  int e, m, p0, rows;       // expert, feature tile, first position, rows up to the last real one
-  int row[kTileRows];       // the row that each position reads, -1: none
+  int e, m, p0, len;        // expert (< 0: no more tiles), feature tile, first position, positions
+  int rows;                 // rows up to the last real one; 0 of padding alone
+  alignas(16) int row[kTileRows];   // the row that each position reads, -1: none
 };
 
 struct Smem {
@@ -113,7 +115,7 @@ struct Smem {
   alignas(128) uint8_t staged[kEpiWarps][32 * 128];    // output on its way out, a warp's own
   alignas(16) TileInfo info[kInfos];
   uint64_t full[kStages], empty[kStages], raw_full[kStages], raw_empty[kStages];
-  uint64_t info_full[kInfos], info_empty[kInfos];
+  uint64_t info_place[kInfos], info_rows[kInfos], info_empty[kInfos];
   uint64_t acc_full, acc_empty, drain;
   int failed;
   uint32_t tmem;
@@ -210,37 +212,22 @@ __device__ __forceinline__ bool wait_all(Smem &S, uint64_t *bar, uint32_t parity
   return __all_sync(kFull, ok);
 }
 
-// Warp 2: the CTA's tiles in order, without those of padding alone.
+// Warp 2: the CTA's tiles in order, each published as soon as its place is known,
+// which is all that the weights' copies need, and again with its rows.
 __device__ void scheduler(const ProductArgs &a, Smem &S, int total) {
   const int lane = threadIdx.x & 31, mt = a.feature_tiles;
   uint32_t n = 0;
-  for (int idx = blockIdx.x;; idx += gridDim.x) {
-    int e = 0, m = 0, p0 = 0, rows = -1, r[4];
+  for (int idx = blockIdx.x;; idx += gridDim.x, ++n) {
+    int e = -1, m = 0, p0 = 0, len = 0;
     if (idx < total) {
-      int hi = a.E - 1;   // e: the last expert whose tiles begin at or ahead of idx
-      while (e < hi) {
-        const int mid = (e + hi + 1) >> 1;
-        if (S.tiles[mid] * mt <= idx)
-          e = mid;
-        else
-          hi = mid - 1;
-      }
+      // the last expert whose tiles begin at or ahead of idx
+      int ahead = 0;
+      for (int i = lane; i < a.E; i += 32) ahead += S.tiles[i] * mt <= idx;
+      e = __reduce_add_sync(kFull, ahead) - 1;
       const int rt = S.tiles[e + 1] - S.tiles[e], at = idx - S.tiles[e] * mt;
       m = at / rt;
       p0 = S.begin[e] + (at - m * rt) * kTileRows;
-      const int len = min(kTileRows, S.begin[e + 1] - p0);
-      rows = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = 4 * lane + j;
-        const int s = i < len ? a.sti[p0 + i] : a.n;
-        r[j] = (unsigned)s >= (unsigned)a.n ? -1 : a.by_token ? s / a.top_k : p0 + i;
-        if (r[j] >= 0) rows = i + 1;
-        if ((s < 0 || s > a.n) && a.err) atomicOr(a.err, MOE_ERR_BAD_POSITION);
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) rows = max(rows, __shfl_xor_sync(kFull, rows, d));
-      if (!rows) continue;
+      len = min(kTileRows, S.begin[e + 1] - p0);
     }
     const int slot = n % kInfos;
     if (n >= kInfos && !wait_all(S, &S.info_empty[slot], (n / kInfos - 1) & 1)) {
@@ -248,29 +235,46 @@ __device__ void scheduler(const ProductArgs &a, Smem &S, int total) {
       return;
     }
     TileInfo &t = S.info[slot];
-    if (lane == 0) *reinterpret_cast<int4 *>(&t.e) = make_int4(e, m, p0, rows);
-    if (rows > 0) *reinterpret_cast<int4 *>(&t.row[4 * lane]) = make_int4(r[0], r[1], r[2], r[3]);
+    if (lane == 0) {
+      *reinterpret_cast<int4 *>(&t.e) = make_int4(e, m, p0, len);
+      mbar_arrive(&S.info_place[slot]);
+    }
+    int rows = 0, r[4];
+    if (e >= 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = 4 * lane + j;
+        const int s = i < len ? a.sti[p0 + i] : a.n;
+        r[j] = (unsigned)s >= (unsigned)a.n ? -1 : !a.by_token ? p0 + i : a.per_k ? (int)__umulhi(s, a.per_k) : s;
+        if (r[j] >= 0) rows = i + 1;
+        if ((s < 0 || s > a.n) && a.err) atomicOr(a.err, MOE_ERR_BAD_POSITION);
+      }
+      rows = __reduce_max_sync(kFull, rows);
+      *reinterpret_cast<int4 *>(&t.row[4 * lane]) = make_int4(r[0], r[1], r[2], r[3]);
+    }
+    if (lane == 0) t.rows = rows;
     __syncwarp();
-    if (lane == 0) mbar_arrive(&S.info_full[slot]);
-    if (rows < 0) return;
-    ++n;
+    if (lane == 0) mbar_arrive(&S.info_rows[slot]);
+    if (e < 0) return;
   }
 }
 
 // A role's view of the tiles: next() gives the next one (NULL at the end, or
-// after a failure, which sets ok = false), done() lets go of it.  Whole warps.
+// after a failure, which sets ok = false), its place alone or with its rows;
+// done() lets go of it.  Whole warps.
 struct Tiles {
   Smem &S;
+  uint64_t *known;
   uint32_t n = 0;
   bool ok = true;
-  __device__ __forceinline__ explicit Tiles(Smem &s) : S(s) {}
+  __device__ __forceinline__ Tiles(Smem &s, bool rows) : S(s), known(rows ? s.info_rows : s.info_place) {}
   __device__ __forceinline__ const TileInfo *next() {
     const TileInfo *t = &S.info[n % kInfos];
-    if (!wait_all(S, &S.info_full[n % kInfos], (n / kInfos) & 1)) {
+    if (!wait_all(S, &known[n % kInfos], (n / kInfos) & 1)) {
       ok = false;
       return nullptr;
     }
-    return t->rows < 0 ? nullptr : t;
+    return t->e < 0 ? nullptr : t;
   }
   __device__ __forceinline__ void done() {
     __syncwarp();
@@ -308,9 +312,9 @@ template <bool kPair>
 __device__ void producer(const ProductArgs &a, const ProductMaps &maps, Smem &S) {
   const int kbs = (a.K + 255) / 256;
   uint32_t s = 0;
-  Tiles tiles(S);
+  Tiles tiles(S, false);
   while (const TileInfo *t = tiles.next()) {
-    const int rows = a.by_token ? 0 : t->rows <= 32 ? 32 : 128, p0 = t->p0;
+    const int rows = a.by_token ? 0 : t->len <= 32 ? 32 : 128, p0 = t->p0;
     const int w0 = t->e * a.R + feature_of<kPair>(t->m, 0);
     tiles.done();
     const uint32_t bytes = 2 * kOperand + rows * 128;
@@ -343,7 +347,7 @@ __device__ void scale_producer(const ProductArgs &a, const ProductMaps &maps, Sm
   const int kbs = a.K / 256;
   const uint32_t bytes = (a.by_token ? 2 : 3) * kRawScales;
   uint32_t s = 0;
-  Tiles tiles(S);
+  Tiles tiles(S, false);
   while (const TileInfo *t = tiles.next()) {
     const int w0 = t->e * a.R + feature_of<kPair>(t->m, 0), p0 = t->p0;
     tiles.done();
@@ -414,12 +418,13 @@ template <bool kPair>
 __device__ void mma_issuer(const ProductArgs &a, Smem &S, uint32_t tmem) {
   const int lane = threadIdx.x & 31, kbs = (a.K + 255) / 256;
   uint32_t s = 0;
-  Tiles tiles(S);
+  Tiles tiles(S, true);
   while (const TileInfo *t = tiles.next()) {
     const int rows = t->rows;
     const bool two = second_half<kPair>(a, t->m), few = rows <= kFewRows;
     tiles.done();
-    const uint32_t id = idesc_nvf4(few ? (rows + 15) / 16 * 16 : two ? 256 : 128);
+    // of padding alone: as a few rows that nothing reads
+    const uint32_t id = idesc_nvf4(few ? max(rows + 15, 16) / 16 * 16 : two ? 256 : 128);
     if (tiles.n > 1 && !wait_all(S, &S.acc_empty, tiles.n & 1)) {
       tiles.ok = false;
       break;
@@ -496,7 +501,7 @@ __device__ void turner(const ProductArgs &a, Smem &S) {
   const int row0 = 4 * warp + (lane >> 3);
   const int pitch = a.K / 16, kbs = a.K / 256;
   uint32_t s = 0;
-  Tiles tiles(S);
+  Tiles tiles(S, true);
   while (const TileInfo *t = tiles.next()) {
     const int words = (t->rows + 31) / 32;
     uint32_t places[8];
@@ -620,7 +625,7 @@ __device__ void copier(const ProductArgs &a, Smem &S) {
   const int first = 32 * j + line, row0 = 4 * warp + (lane >> 3);
   const int pitch = a.K / 16, kbs = (a.K + 255) / 256;
   uint32_t s = 0;
-  Tiles tiles(S);
+  Tiles tiles(S, true);
   while (const TileInfo *t = tiles.next()) {
     const int rows = t->rows;
     int64_t w[2];
@@ -764,7 +769,7 @@ __device__ void epilogue(const ProductArgs &a, Smem &S, uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3;
   const int group = (warp - kEpi0) >> 2;
   const uint32_t base = tmem + ((uint32_t)(q * 32) << 16);
-  Tiles tiles(S);
+  Tiles tiles(S, true);
   while (const TileInfo *t = tiles.next()) {
     const int rows = t->rows, m = t->m, p0 = t->p0;
     const bool few = rows <= kFewRows;
@@ -862,7 +867,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.raw_empty[i], 4);
     }
     for (int i = 0; i < kInfos; ++i) {
-      mbar_init(&S.info_full[i], 1);
+      mbar_init(&S.info_place[i], 1);
+      mbar_init(&S.info_rows[i], 1);
       mbar_init(&S.info_empty[i], 2 + kTmaScales + 4 + kEpiWarps);
     }
     mbar_init(&S.acc_full, 1);
@@ -1009,7 +1015,7 @@ int grouped(const moe_proj *w0, const moe_proj *w1, int E, int R, int K, const u
   a.R = R;
   a.K = K;
   a.by_token = by_token;
-  a.top_k = top_k;
+  a.per_k = top_k == 1 ? 0 : (uint32_t)(((uint64_t)1 << 32) / top_k + ((((uint64_t)1 << 32) % top_k) != 0));
   a.n = M * top_k;
   a.num_rows = num_rows;
   a.x_rows = by_token ? M : num_rows;
