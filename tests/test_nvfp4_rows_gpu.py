@@ -620,3 +620,106 @@ def test_straight_through_gradient():
     # two fp32 products in the gradient, and the differences' cancellation in float64
     tol = 4 * U * diff.abs() + 2.0 ** -52 * (v.square() + 1) * c.abs() / step
     assert ((x.grad.double() - diff).abs() <= tol).all()
+
+
+# --------------------------------------------------------------------------
+# sizes and uses at the ends
+# --------------------------------------------------------------------------
+
+def test_two_products_at_once():
+    """Two streams with products of their own on the same weights."""
+    g = gen(41)
+    w, up = weights(g, 6, 640, 512), weights(g, 6, 640, 512)
+    t, n = align([200, 3, 0, 90, 1, 300], 16)
+    x = moe.moe_quantize_nvfp4(randn(g, n, 512, dtype=BF))
+    one = moe.moe_grouped_gate_up_nvfp4(w, up, x, t, 1, out=torch.zeros(
+        t["max_total"], 640, dtype=BF, device="cuda"))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.zeros_like(one) for _ in streams]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for s, o in zip(streams, outs):
+            moe.moe_grouped_gate_up_nvfp4(w, up, x, t, 1, out=o, stream=s)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, one)
+
+
+def test_products_repeat_to_the_bit():
+    g = gen(42)
+    w = weights(g, 5, 1000, 1120)
+    t, n = align([700, 0, 33, 32, 129], 1)
+    x = moe.moe_quantize_nvfp4(randn(g, n, 1120, dtype=BF))
+    first = moe.moe_grouped_product_nvfp4(w, x, t, 1, out_dtype=FL)
+    for _ in range(50):
+        assert torch.equal(moe.moe_grouped_product_nvfp4(w, x, t, 1, out_dtype=FL), first)
+
+
+def test_outputs_at_any_element_address():
+    """Outputs whose rows no 16-byte piece fits."""
+    for dtype, R, by_token in ((BF, 130, True), (HF, 256, False), (FL, 96, True), (FL, 257, False)):
+        g = gen(R)
+        t, n = align([70, 5, 140], 16)
+        w = weights(g, 3, R, 256)
+        x = moe.moe_quantize_nvfp4(randn(g, n if by_token else t["max_total"], 256, dtype=BF))
+        M = None if by_token else n
+        flat = torch.full((t["max_total"] * R + 1,), 5.0, dtype=dtype, device="cuda")
+        moe.moe_grouped_product_nvfp4(w, x, t, 1, M=M, out=flat[1:].view(-1, R))
+        p, at, e = rows_of(t, 1, by_token)
+        y, mag = sums(x, w, at, e)
+        check_product(flat[1:].view(-1, R)[p], y, (256 * 2.0 ** -23 + 2 * U) * mag, 256)
+        rest = torch.ones(t["max_total"], dtype=torch.bool, device="cuda")
+        rest[p] = False
+        assert bool((flat[1:].view(-1, R)[rest] == 5.0).all()) and float(flat[0]) == 5.0
+
+
+def test_scales_of_any_width_at_the_arrays_ends():
+    """Rows of scales that are no whole words or pieces: the last row of the last
+    expert, the last token."""
+    for C in (32, 96, 160, 288, 352, 64, 192, 320):
+        for R in (1, 3, 97, 129, 193):
+            run_product([2, 40, 1], R, C, BS=1, seed=C + R, dtype=FL)
+
+
+def test_weights_beyond_four_gigabytes():
+    E, R, C = 600, 8192, 2048
+    codes = torch.randint(0, 256, (E, R, C // 2), dtype=torch.uint8, device="cuda",
+                          generator=gen(50))
+    scale = torch.randint(0x28, 0x40, (E, R, C // 16), dtype=torch.uint8, device="cuda",
+                          generator=gen(51))
+    glob = torch.full((E,), 0.01, device="cuda")
+    ids = torch.tensor([[0], [599], [598], [599], [300]], dtype=torch.int32, device="cuda")
+    t = moe.moe_align(ids, E, 1)
+    x = moe.moe_quantize_nvfp4(randn(gen(52), 5, C, dtype=BF))
+    y = moe.moe_grouped_product_nvfp4((codes, scale, glob), x, t, 1, out_dtype=FL)
+    got = y[t["token_to_perm"].long()]
+    X = wide(x)
+    for i, e in enumerate(ids.view(-1).tolist()):
+        W = wide((codes[e], scale[e], glob[e].expand(R)))
+        check_product(got[i: i + 1], (X[i] @ W.T)[None],
+                      ((C * 2.0 ** -23 + 2 * U) * (X[i].abs() @ W.abs().T))[None], C)
+
+
+def test_rows_beyond_two_billion_elements():
+    M, H = 270001, 8192
+    x = torch.empty(M, H, dtype=BF, device="cuda").normal_(generator=gen(60))
+    q = moe.moe_quantize_nvfp4(x)
+    pick = torch.tensor([0, 1, 131072, 262143, 262144, M - 2, M - 1], device="cuda")
+    check_quantized({n: v[pick] for n, v in q.items()}, x[pick])
+    got = moe.moe_dequantize_nvfp4(q["codes"], q["scale"], q["global_scale"])
+    same(got[pick], ref_quantize(x[pick])[3].to(BF))
+    m = x[:262144].view(2, 131072, H)
+    q = moe.moe_quantize_nvfp4(m)
+    tail = m[1, -3:]
+    check_quantized({"codes": q["codes"][1, -3:], "scale": q["scale"][1, -3:],
+                     "global_scale": q["global_scale"][1:].expand(3)}, tail,
+                    q["global_scale"][1:].expand(3))
+    top = m[1].abs().amax().double() / torch.full((), 2688.0, dtype=torch.float64, device="cuda")
+    assert float(q["global_scale"][1]) == float(top.float())
+
+
+def test_a_single_row_and_a_single_expert():
+    for C, R in ((32, 1), (16384, 5), (16384, 300)):
+        run_product([1], R, C, BS=1, seed=C + R, dtype=FL)
+    run_product([65], 65536, 64, BS=1, seed=9)
