@@ -15,22 +15,21 @@
 //  * A tile is up to 128 rows by 256 weight rows: 128 features of gate and of
 //    up, or 256 neighbours of one matrix.  With many rows the tokens are the
 //    MMA's 128 lanes and the weights its 256 columns, so that a thread of the
-//    epilogue has neighbouring features of one row and stores whole sectors.
-//    With few the weights are the lanes and the tokens the columns (16 or 32):
-//    the epilogue is as short as the rows are few.  Both read the same shared
-//    memory and the same scales.
-//  * A stage is 256 k: 128 bytes a row, the width of the swizzle.  Weight
-//    tiles come by TMA boxes, and so do rows in expert order; the tokens' own
-//    rows, which can be any, by 16-byte copies (cp.async) that
-//    place them as the swizzle would, so that tokens need not be copied into
-//    expert order first.  (TMA gathers of four rows each took the gate and up
-//    of 4096 rows from 91 to 150 us.)
+//    epilogue has neighbouring features of one row.  With few (32 or fewer) the
+//    weights are the lanes and the tokens the columns: the epilogue is as short
+//    as the rows are few.  Both read the same shared memory and the same scales.
+//  * A stage is 256 k: 128 bytes a row, the width of the swizzle.  Weight tiles
+//    come by TMA boxes, and so do rows in expert order; the tokens' own rows,
+//    which can be any, by 16-byte copies (cp.async) that place them as the
+//    swizzle would, so that tokens need not be copied into expert order first.
+//    (TMA gathers of four rows each took the gate and up of 4096 rows from 91 to
+//    150 us.)
 //  * Scales stay row-major as the format has them.  TMA brings a stage's 16
 //    bytes a row, and four warps turn them by words of 4 blocks (64 k) to where
 //    the tensor cores' own copy to tensor memory takes them (tcgen05.cp 32x128b,
 //    issued ahead of the stage's MMAs): for each 64 k and 128 rows 32 x 16 bytes,
 //    line = row % 32, word = row / 32.  Rows of scales that TMA does not take (k
-//    no multiple of 256) the four warps copy there by words.
+//    no multiple of 256) the four warps copy there themselves.
 //  * A persistent CTA an SM walks over (expert, feature tile, row tile), the
 //    row tiles innermost: CTAs next to one another share weights, and an
 //    expert's rows stay in L2.
@@ -38,8 +37,23 @@
 //    run further ahead, warp 1 issues MMAs, warp 2 looks the tiles up ahead of
 //    all others, warps 4-7 turn the scales and copy tokens' rows, warps 8-15 are
 //    the epilogue, which takes the accumulators into registers first, so that
-//    the next tile's MMAs run beside its arithmetic and stores.  The roles meet at mbarriers alone;
-//    every wait gives up after about two seconds with MOE_ERR_TIMEOUT.
+//    the next tile's MMAs run beside its arithmetic and stores.  The roles meet
+//    at mbarriers alone; every wait gives up after about two seconds with
+//    MOE_ERR_TIMEOUT.
+//
+// Measured and bounds (one GB300; E experts, k an expert's input width):
+//  * Few rows an expert: HBM.  128 tokens, 199 of 256 experts active, 4096 x 1536
+//    gate and up (1.41 GB read): 205-216 us, 6.6-6.9 TB/s.
+//  * Many: shared memory and the ring.  An MMA of 256 columns and 64 k takes 128
+//    clocks and reads 12 KB of the 128 bytes a clock that shared memory gives, and
+//    the copies write as much: with them a stage takes about 790 clocks instead of
+//    512, and three stages (all that fits) do not hide a copy's 2000.  Gate and up
+//    of 4096 tokens (128 experts, 2048 x 768, 206 GFLOP) 80 us, 2.6 PFLOP/s; down
+//    of 8192 (256 experts, 1536 x 4096, 825 GFLOP, 1.5 GB) 304 us, 2.7.  Two stages
+//    take 359 us there; tiles of 192 columns, whose accumulators tensor memory
+//    holds twice, 365; codes brought to L2 ahead, 333.
+//  * One token: its chain of latencies, 8.8 us (8 experts, 14 MB): 1 us to the
+//    first tile's place, 1 to its first copies, eight stages of 0.45, the epilogue.
 #include <atomic>
 #include <cstring>
 
@@ -158,9 +172,9 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
 }
 // One lane of a converged warp, the same one every time.  MMAs and copies are
 // issued under it and unrolled: the compiler knows of it that one lane is
-// active, and keeps descriptors in uniform registers.  (Under lane == 0 every
-// issue took 180 clocks, with it in a rolled loop 150; unrolled an MMA of 256
-// columns takes the tensor cores' own 128, and a copy of scales beside it none.)
+// active.  (In a rolled loop under lane == 0 an MMA took 180 to 190 clocks to issue,
+// under this 150; unrolled one of 256 columns takes the tensor cores' own 128, and
+// a copy of scales beside it none.)
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(
@@ -697,7 +711,8 @@ __device__ void copier(const ProductArgs &a, Smem &S) {
 }
 
 __device__ __forceinline__ float silu_times(float g, float u) {
-  return __fdividef(g, 1.f + expf(-g)) * u;   // at most 2^126: 0 beyond, where it is below 2^-119
+  // a denominator over 2^126 gives 0, for what is below 2^-119
+  return __fdividef(g, 1.f + expf(-g)) * u;
 }
 
 template <typename T>
@@ -714,7 +729,7 @@ __device__ __forceinline__ void store_one(void *out, int64_t at, float v) {
 // of row r goes to c ^ (r % 8), so that neither side of the exchange has bank
 // conflicts.  (Straight to global memory, a warp's store is 32 rows of 32 bytes:
 // that took the stores' pipe 125 clocks and held up every other copy; down of
-// 8192 rows 390 us.)
+// 8192 rows 390 us, staged 310.)
 template <typename T>
 __device__ __forceinline__ void stage_outputs(uint8_t *rows, int lane, int half,
                                               const uint32_t (&v)[32]) {

@@ -638,7 +638,7 @@ size_t moe_quantize_nvfp4_workspace_bytes(int groups, int rows, int cols);
  *   least moe_quantize_nvfp4_workspace_bytes; needs no clearing, and calls
  *   that overlap on the GPU need one each.
  * groups = 0 is valid.  cols: a multiple of 16 up to MOE_MAX_ROW_HIDDEN; rows
- * of whole 16-byte pieces, 16-byte aligned, are the fast ones.  Outputs overlap
+ * aligned to 32 bytes are the fast ones, then those aligned to 16.  Outputs overlap
  * no input, but values may be x's own buffer when x is dense.
  * Errors: MOE_EINVAL (NULL, sizes, strides, types, misaligned: codes 8 bytes,
  * others their elements; a missing or short workspace; values on a strided
