@@ -52,8 +52,9 @@
 //    of 8192 (256 experts, 1536 x 4096, 825 GFLOP, 1.5 GB) 304 us, 2.7.  Two stages
 //    take 359 us there; tiles of 192 columns, whose accumulators tensor memory
 //    holds twice, 365; codes brought to L2 ahead, 333.
-//  * One token: its chain of latencies, 8.8 us (8 experts, 14 MB): 1 us to the
-//    first tile's place, 1 to its first copies, eight stages of 0.45, the epilogue.
+//  * One token: its chain of latencies, 8.3 us (8 experts, 14 MB): 1 us to the
+//    first tile's place, 1 to its first copies, eight stages of 0.45, which the
+//    MMAs' issue bounds, the epilogue.
 #include <atomic>
 #include <cstring>
 
@@ -133,7 +134,6 @@ struct Smem {
   uint64_t acc_full, acc_empty, drain;
   int failed;
   uint32_t tmem;
-  int warp_sum[kWarps];
   int tiles[MOE_MAX_EXPERTS + 1];   // row tiles ahead of each expert's
   int begin[MOE_MAX_EXPERTS + 1];   // the runs' first positions
 };
@@ -226,9 +226,50 @@ __device__ __forceinline__ bool wait_all(Smem &S, uint64_t *bar, uint32_t parity
   return __all_sync(kFull, ok);
 }
 
-// Warp 2: the CTA's tiles in order, each published as soon as its place is known,
+// Warp 2 alone looks at the tables: S.tiles, the row tiles ahead of each expert's, and
+// the runs' first positions; returns the number of tiles, 0 for tables that are
+// none (their tiles could be any number).
+__device__ __forceinline__ int lay_out_tiles(const ProductArgs &a, Smem &S) {
+  constexpr int U = 4;   // neighbouring experts of a lane
+  const int lane = threadIdx.x & 31;
+  int ahead = 0, bad = 0;
+#pragma unroll 1
+  for (int e = lane * U; e - lane * U < a.E; e += 32 * U) {
+    int at[U + 1], before[U + 1];
+#pragma unroll
+    for (int u = 0; u <= U; ++u) at[u] = a.offsets[min(e + u, a.E)];
+    before[0] = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int wrong = at[u] < 0 || at[u + 1] < at[u] || at[u + 1] > a.num_rows;
+      bad |= wrong;
+      before[u + 1] =
+          before[u] + (wrong ? 0 : (at[u + 1] - at[u] + kTileRows - 1) / kTileRows);
+    }
+    int inc = before[U];
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int v = __shfl_up_sync(kFull, inc, k);
+      if (lane >= k) inc += v;
+    }
+    const int first = ahead + inc - before[U];
+#pragma unroll
+    for (int u = 0; u <= U; ++u)
+      if (e + u <= a.E) {   // the entry behind the last too; a neighbour writes the same
+        S.tiles[e + u] = first + before[u];
+        S.begin[e + u] = at[u];
+      }
+    ahead += __shfl_sync(kFull, inc, 31);
+  }
+  __syncwarp();
+  bad = __reduce_or_sync(kFull, bad);
+  if (bad && a.err && lane == 0) atomicOr(a.err, MOE_ERR_BAD_POSITION);
+  return bad ? 0 : ahead * a.feature_tiles;
+}
+
+// The CTA's tiles in order, each published as soon as its place is known,
 // which is all that the weights' copies need, and again with its rows.
-__device__ void scheduler(const ProductArgs &a, Smem &S, int total) {
+__device__ __forceinline__ void scheduler(const ProductArgs &a, Smem &S, int total) {
   const int lane = threadIdx.x & 31, mt = a.feature_tiles;
   uint32_t n = 0;
   for (int idx = blockIdx.x;; idx += gridDim.x, ++n) {
@@ -900,46 +941,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (warp == 0 && lane < (kPair ? 2 : 1)) prefetch_tensormap(&maps.w[lane]);
+  if (warp == 3 && kTmaScales && lane < (kPair ? 2 : 1)) prefetch_tensormap(&maps.ws[lane]);
+  if (warp == 3 && !a.by_token && lane >= 8 && lane < 10) prefetch_tensormap(&maps.x[lane - 8]);
+  if (warp == 3 && !a.by_token && kTmaScales && lane == 10) prefetch_tensormap(&maps.xs);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S.tmem;
   pdl_wait();
   pdl_trigger();
-
-  // S.tiles: the row tiles ahead of each expert's, a thread's two experts at a time
-  int run[2], bad = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int e = 2 * threadIdx.x + i;
-    run[i] = 0;
-    if (e < a.E) {
-      const int b = a.offsets[e], d = a.offsets[e + 1];
-      S.begin[e] = b;
-      if (e == a.E - 1) S.begin[a.E] = d;
-      bad |= b < 0 || d < b || d > a.num_rows;
-      run[i] = d > b && !bad ? (d - b + kTileRows - 1) / kTileRows : 0;
-    }
-  }
-  // tables that are none: nothing is computed (their tiles could be any number)
-  const bool refused = __syncthreads_or(bad);
-  if (refused && a.err && threadIdx.x == 0) atomicOr(a.err, MOE_ERR_BAD_POSITION);
-  int inc = run[0] + run[1];
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int v = __shfl_up_sync(kFull, inc, d);
-    if (lane >= d) inc += v;
-  }
-  if (lane == 31) S.warp_sum[warp] = inc;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) inc += S.warp_sum[w];
-  if (2 * (int)threadIdx.x < a.E) {
-    S.tiles[2 * threadIdx.x + 1] = inc - run[1];
-    if (2 * (int)threadIdx.x + 1 < a.E) S.tiles[2 * threadIdx.x + 2] = inc;
-  }
-  if (threadIdx.x == 0) S.tiles[0] = 0;
-  __syncthreads();
-  const int total = refused ? 0 : S.tiles[a.E] * a.feature_tiles;
 
   if (warp >= kEpi0) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
@@ -957,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (warp == 1)
       mma_issuer<kPair>(a, S, tmem);
     else if (warp == 2)
-      scheduler(a, S, total);
+      scheduler(a, S, lay_out_tiles(a, S));
     else if (kTmaScales)
       scale_producer<kPair>(a, maps, S);
   }

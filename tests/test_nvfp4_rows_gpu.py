@@ -21,6 +21,9 @@ finfo(T).eps / 2 the rounding to T):
 from __future__ import annotations
 
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -723,3 +726,56 @@ def test_a_single_row_and_a_single_expert():
     for C, R in ((32, 1), (16384, 5), (16384, 300)):
         run_product([1], R, C, BS=1, seed=C + R, dtype=FL)
     run_product([65], 65536, 64, BS=1, seed=9)
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls of these entry points are inside a capture."""
+    code = """
+import torch, expert_routing_alignment_gb300 as moe
+moe.load()
+torch.manual_seed(0)
+M, H, I, E, k = 40, 512, 256, 8, 2
+x = torch.randn(M, H, device="cuda").bfloat16()
+wide = [torch.randn(E, *s, device="cuda").bfloat16() for s in ((I, H), (I, H), (H, I))]
+ids, tw = moe.moe_topk_softmax(torch.randn(M, E, device="cuda"), k)
+t = moe.moe_align(ids, E, 16)
+def run():
+    g, u, d = ((q["codes"], q["scale"], q["global_scale"]) for q in
+               map(moe.moe_quantize_nvfp4, wide))
+    q = moe.moe_quantize_nvfp4(x)
+    h = moe.moe_grouped_gate_up_nvfp4(g, u, q, t, k)
+    hq = moe.moe_quantize_nvfp4(h, tables=t)
+    y = moe.moe_grouped_product_nvfp4(d, hq, t, k, M=M)
+    return moe.moe_combine(y, tw, t), moe.moe_dequantize_nvfp4(*d)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+for a, b in zip(got, run()):
+    assert torch.equal(a, b)
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root,
+                       timeout=300)
+    assert p.returncode == 0 and "same" in p.stdout, p.stdout + p.stderr
+
+
+def test_tables_of_a_layer_call():
+    """The tables that a layer call leaves in its workspace serve the products."""
+    import synth
+    shape = synth.tiny()
+    dev = synth.make_layer(shape, 7, device="cpu").to("cuda")
+    layer = moe.LayerDesc(top_k=shape.top_k, block_size=shape.BS,
+                          routed=moe.Experts.from_synth(dev.experts))
+    ws = moe.alloc_workspace(layer, shape.M)
+    out = torch.empty(shape.M, shape.H, dtype=BF, device="cuda")
+    moe.moe_decode_layer(layer, dev.x, out, ws, router_logits=dev.logits)
+    v = moe.workspace_view(layer, shape.M, ws)
+    w = weights(gen(3), shape.E, 96, shape.H)
+    x = moe.moe_quantize_nvfp4(dev.x)
+    got = moe.moe_grouped_product_nvfp4(w, x, v, shape.top_k, out_dtype=FL)
+    p, at, e = rows_of(v, shape.top_k, True)
+    y, mag = sums(x, w, at, e)
+    check_product(got[p], y, (shape.H * 2.0 ** -23 + 2 * U) * mag, shape.H)
