@@ -267,13 +267,29 @@ __device__ __forceinline__ int lay_out_tiles(const ProductArgs &a, Smem &S) {
   return bad ? 0 : ahead * a.feature_tiles;
 }
 
-// The CTA's tiles in order, each published as soon as its place is known,
-// which is all that the weights' copies need, and again with its rows.
+// The CTA's tiles in order.  A run's first tile is published as soon as its place
+// is known, which is all that the weights' copies need, and again with its rows;
+// later ones, of which those of padding alone are left out, with their rows.
 __device__ __forceinline__ void scheduler(const ProductArgs &a, Smem &S, int total) {
   const int lane = threadIdx.x & 31, mt = a.feature_tiles;
   uint32_t n = 0;
-  for (int idx = blockIdx.x;; idx += gridDim.x, ++n) {
-    int e = -1, m = 0, p0 = 0, len = 0;
+  for (int idx = blockIdx.x;; idx += gridDim.x) {
+    int e = -1, m = 0, p0 = 0, len = 0, rows = 0, r[4];
+    bool looked = false;
+    auto look = [&] {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = 4 * lane + j;
+        const int s = i < len ? a.sti[p0 + i] : a.n;
+        r[j] = (unsigned)s >= (unsigned)a.n ? -1
+               : !a.by_token                ? p0 + i
+               : a.per_k                    ? (int)__umulhi(s, a.per_k)
+                                            : s;
+        if (r[j] >= 0) rows = i + 1;
+        if ((s < 0 || s > a.n) && a.err) atomicOr(a.err, MOE_ERR_BAD_POSITION);
+      }
+      rows = __reduce_max_sync(kFull, rows);
+    };
     if (idx < total) {
       // the last expert whose tiles begin at or ahead of idx
       int ahead = 0;
@@ -283,6 +299,11 @@ __device__ __forceinline__ void scheduler(const ProductArgs &a, Smem &S, int tot
       m = at / rt;
       p0 = S.begin[e] + (at - m * rt) * kTileRows;
       len = min(kTileRows, S.begin[e + 1] - p0);
+      looked = at != m * rt;
+      if (looked) {
+        look();
+        if (!rows) continue;
+      }
     }
     const int slot = n % kInfos;
     if (n >= kInfos && !wait_all(S, &S.info_empty[slot], (n / kInfos - 1) & 1)) {
@@ -294,23 +315,15 @@ __device__ __forceinline__ void scheduler(const ProductArgs &a, Smem &S, int tot
       *reinterpret_cast<int4 *>(&t.e) = make_int4(e, m, p0, len);
       mbar_arrive(&S.info_place[slot]);
     }
-    int rows = 0, r[4];
     if (e >= 0) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = 4 * lane + j;
-        const int s = i < len ? a.sti[p0 + i] : a.n;
-        r[j] = (unsigned)s >= (unsigned)a.n ? -1 : !a.by_token ? p0 + i : a.per_k ? (int)__umulhi(s, a.per_k) : s;
-        if (r[j] >= 0) rows = i + 1;
-        if ((s < 0 || s > a.n) && a.err) atomicOr(a.err, MOE_ERR_BAD_POSITION);
-      }
-      rows = __reduce_max_sync(kFull, rows);
+      if (!looked) look();
       *reinterpret_cast<int4 *>(&t.row[4 * lane]) = make_int4(r[0], r[1], r[2], r[3]);
     }
     if (lane == 0) t.rows = rows;
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.info_rows[slot]);
     if (e < 0) return;
+    ++n;
   }
 }
 

@@ -779,3 +779,20 @@ def test_tables_of_a_layer_call():
     p, at, e = rows_of(v, shape.top_k, True)
     y, mag = sums(x, w, at, e)
     check_product(got[p], y, (shape.H * 2.0 ** -23 + 2 * U) * mag, shape.H)
+
+
+def test_long_padded_runs():
+    """Blocks of many tiles, of which few have a row; and runs whose real rows do
+    not come first (tables of the user's own)."""
+    run_product([3, 0, 300, 1], 160, 256, BS=1000, seed=70)
+    run_product([3, 0, 300, 1], 160, 288, BS=700, by_token=False, seed=71, dtype=FL)
+    t, n = align([40, 20], 400)
+    ids = t["sorted_token_ids"].clone()
+    ids[:400] = ids[:400].flip(0)     # expert 0: its rows at the run's end
+    t2 = {**t, "sorted_token_ids": ids}
+    g = gen(72)
+    w, x = weights(g, 2, 96, 128), moe.moe_quantize_nvfp4(randn(g, n, 128, dtype=BF))
+    a = moe.moe_grouped_product_nvfp4(w, x, t, 1, out=torch.zeros(
+        t["max_total"], 96, device="cuda"))
+    b = moe.moe_grouped_product_nvfp4(w, x, t2, 1, out=torch.zeros_like(a))
+    assert torch.equal(b[:400], a[:400].flip(0)) and torch.equal(b[400:], a[400:])
