@@ -13,8 +13,8 @@
 // Rows: x is read once; 8192 x 4096 bf16 with values (153 MB) 24.0 us, 6.4 TB/s,
 // bound by HBM and, nearly, by issue.  Matrices: read twice, for the maximum and
 // for the codes; 32 x 1536 x 2048 bf16 with values (459 MB, 660 with the second
-// read) 110 us.  (Read once, held in the shared memory of CTAs that meet at the
-// maximum: 143 us, each meeting 4.5; in turns that find x in L2: 111.)  The
+// read) 104 us.  (Read once, held in the shared memory of CTAs that meet at the
+// maximum: 143 us, each meeting 4.5; in turns that find x in L2: no faster.)  The
 // inverse: 64 x 768 x 2048 to bf16 (258 MB) 39.7 us, 6.5 TB/s.
 #include "nvfp4.cuh"
 
@@ -23,7 +23,6 @@ namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kThreads = 256;
-constexpr int kMostParts = 128;   // parts of a group's maximum
 
 struct PackArgs {
   const void *x;
@@ -155,7 +154,7 @@ __global__ void __launch_bounds__(kThreads)
     g = a.given[blockIdx.y];
   } else {
     float top = 0.f;
-    if ((int)threadIdx.x < parts) top = part[blockIdx.y * parts + threadIdx.x];
+    for (int i = threadIdx.x; i < parts; i += kThreads) top = fmaxf(top, part[blockIdx.y * parts + i]);
     g = global_of(cta_max(top));
   }
   if (a.global && blockIdx.x == 0 && threadIdx.x == 0) a.global[blockIdx.y] = g;
@@ -239,12 +238,19 @@ int pack_sizes(int groups, int rows, int cols) {
   return MOE_OK;
 }
 
-// CTAs of a group, so that all of them are a few for each SM.
+// Parts of a group's maximum at most, a bound on the CTAs of a group.
+int most_parts(int groups) {
+  const int parts = groups > 0 ? 4096 / groups : 1;
+  return parts < 1 ? 1 : parts > 1024 ? 1024 : parts;
+}
+// CTAs of a group: 24 for each SM in all, three times what is resident, so that the
+// last ones are short (32 x 1536 x 2048 bf16 with values 104 us, 8 an SM 110).
 int group_parts(int groups, int rows, int cols) {
   const int64_t most = ceil_div64((int64_t)rows * (cols / kBlock16), kThreads);
-  int64_t parts = ceil_div64((int64_t)sm_count() * 8, groups);
+  int64_t parts = (int64_t)sm_count() * 24 / groups;
   if (parts > most) parts = most;
-  return (int)(parts < 1 ? 1 : parts > kMostParts ? kMostParts : parts);
+  if (parts > most_parts(groups)) parts = most_parts(groups);
+  return (int)(parts < 1 ? 1 : parts);
 }
 
 }  // namespace
@@ -253,7 +259,7 @@ int group_parts(int groups, int rows, int cols) {
 extern "C" size_t moe_quantize_nvfp4_workspace_bytes(int groups, int rows, int cols) {
   using namespace moe;
   if (pack_sizes(groups, rows, cols)) return 0;
-  return rows == 1 ? 16 : ((size_t)groups * kMostParts * 4 + 15) / 16 * 16 + 16;
+  return rows == 1 ? 16 : ((size_t)groups * most_parts(groups) * 4 + 15) / 16 * 16 + 16;
 }
 
 extern "C" int moe_quantize_nvfp4(const void *x, int64_t x_stride, int dtype, int groups, int rows,
@@ -315,7 +321,7 @@ extern "C" int moe_quantize_nvfp4(const void *x, int64_t x_stride, int dtype, in
         if (values) b.values = static_cast<char *>(values) + r0 * cols * eb;
         if (global_scale) b.global = global_scale + g0;
         if (given_scale) b.given = given_scale + g0;
-        float *part = static_cast<float *>(workspace) + (int64_t)g0 * kMostParts;
+        float *part = static_cast<float *>(workspace) + (int64_t)g0 * most_parts(groups);
         if (!given_scale)
           if (const int st = launch_pdl(group_max_kernel<T, A>, dim3(parts, gn), dim3(kThreads), 0,
                                         stream, b, rows, part))
