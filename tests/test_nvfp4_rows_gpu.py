@@ -154,6 +154,22 @@ def test_expert_matrices(dtype, E, R, C):
     check_quantized(moe.moe_quantize_nvfp4(x, want=ALL), x)
 
 
+@pytest.mark.parametrize("at", [0, 1, 300000, 8388600, 8388607])
+def test_one_large_matrix_finds_its_maximum_anywhere(at):
+    """More parts of the maximum than a CTA has threads."""
+    x = randn(gen(7), 1, 4096, 2048, dtype=BF, scale=0.02)
+    x.view(-1)[at] = -9.0
+    q = moe.moe_quantize_nvfp4(x, want=ALL)
+    assert float(q["global_scale"][0]) == float(torch.tensor(9.0) / torch.tensor(2688.0))
+    check_quantized(q, x)
+
+
+@pytest.mark.parametrize("groups", [4096, 4097, 70000])
+def test_many_small_matrices(groups):
+    x = randn(gen(groups), groups, 2, 16)
+    check_quantized(moe.moe_quantize_nvfp4(x, want=ALL), x)
+
+
 def test_every_tie_of_a_code_and_of_a_scale():
     """Steps that are powers of two and of other E4M3 values, elements on each
     border between two codes and next to it."""
