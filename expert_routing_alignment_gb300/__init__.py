@@ -268,7 +268,8 @@ def alloc_align_outputs(n: int, num_experts: int, block_size: int, device="cuda"
 def moe_align(topk_ids: torch.Tensor, num_experts: int, block_size: int,
               out: Optional[dict] = None, err_word: Optional[torch.Tensor] = None,
               stream=None) -> dict:
-    """Alignment tables of the flat ids (int32 or int64, device)."""
+    """Alignment tables of the flat ids (int32 or int64, device), with their
+    number as "num_slots" (buffers of ``out`` may be larger)."""
     ids = topk_ids.contiguous().view(-1)
     n = ids.numel()
     if out is None:
@@ -279,6 +280,7 @@ def moe_align(topk_ids: torch.Tensor, num_experts: int, block_size: int,
         _ptr(out["expert_offsets"]), _ptr(out["token_to_perm"]), _ptr(out["active_experts"]),
         _ptr(out["active_count"]), _ptr(out["num_tokens_post_padded"]), _ptr(err_word),
         _stream(stream)))
+    out["num_slots"] = n
     return out
 
 
@@ -558,6 +560,16 @@ def _num_rows(tables: dict) -> int:
     """Rows of the expert-order buffers: the tables' max_total."""
     n = tables["sorted_token_ids"].numel()
     return min(n, tables.get("max_total", n))
+
+
+def _num_slots(tables: dict) -> Optional[int]:
+    """The slots that the tables are of, which is also the slot that padding
+    positions hold: moe_align's count, or as many as token_to_perm has."""
+    n = tables.get("num_slots")
+    if n is None:
+        ttp = tables.get("token_to_perm")
+        n = None if ttp is None else ttp.numel()
+    return n
 
 
 def _err(err_word: Optional[torch.Tensor]):
@@ -952,7 +964,9 @@ def moe_quantize_nvfp4(x: torch.Tensor, want: Sequence[str] = ("codes", "scale",
         sti = tables["sorted_token_ids"]
         if rows != 1 or len(shape) == 3 or _num_rows(tables) != groups:
             raise ValueError(f"x: want the tables' {_num_rows(tables)} rows, got {shape}")
-        s_at, n = _table("sorted_token_ids", sti, groups), tables["token_to_perm"].numel()
+        s_at, n = _table("sorted_token_ids", sti, groups), _num_slots(tables)
+        if n is None:
+            raise ValueError("tables: want num_slots or token_to_perm, the slots they are of")
     if global_scale is not None:
         g_at = _at("global_scale", global_scale, _F32, (groups,))
     at = {}
@@ -1027,6 +1041,9 @@ def _grouped_nvfp4(fn: str, sets: tuple, rows, tables: dict, top_k: int, M: Opti
     by_token, n_rows = M is None, _num_rows(tables)
     if by_token:
         M = codes.shape[0]
+    slots = _num_slots(tables)
+    if slots is not None and M * top_k != slots:
+        raise ValueError(f"want the {slots} slots of the tables, got {M} tokens of {top_k}")
     n = M if by_token else n_rows
     x_at = _packed_at("rows", x, (n, C // 2), (n, C // 16))
     offs, sti = tables["expert_offsets"], tables["sorted_token_ids"]
@@ -1056,9 +1073,9 @@ def moe_grouped_product_nvfp4(weight, rows, tables: dict, top_k: int, M: Optiona
     weight (codes [E, R, C / 2], scale, global_scale) and rows (the same of
     moe_quantize_nvfp4, as its dict or in that order), four bits both.  Without
     M the rows are the tokens' own, read through the tables; with M, the number
-    of tokens, they are in expert order, [max_total, C].  out has out_dtype
-    (bf16 by default); its padding rows stay as they were (undefined in a new
-    buffer)."""
+    of tokens, they are in expert order, [max_total, C].  The tables are those of
+    as many tokens and top_k.  out has out_dtype (bf16 by default); its padding
+    rows stay as they were (undefined in a new buffer)."""
     return _grouped_nvfp4("moe_grouped_product_nvfp4", (weight,), rows, tables, top_k, M, out,
                           out_dtype, err_word, stream)
 

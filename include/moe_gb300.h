@@ -668,7 +668,9 @@ int moe_dequantize_nvfp4(const uint8_t *codes, const uint8_t *scale,
  * weight: the matrices [num_experts][out_dim][in_dim] (one moe_proj in
  * NVFP4_G16), codes, scale, global_scale: the rows, [M][in_dim] by token or
  * [num_rows][in_dim] in expert order.  expert_offsets, sorted_token_ids and
- * num_rows (the tables' max_total) as moe_align writes them for n = M * top_k.
+ * num_rows (the tables' max_total) as moe_align writes them for n = M * top_k
+ * (tables of another n: the slot n that marks their padding may be taken for a
+ * real one, or real ones for padding).
  *   out [num_rows][out_dim] of out_dtype (BF16, F16, F32): rows of real
  *   positions are written, all others stay as they were.
  * The product of a gradient with the experts' weights is the same call on a
