@@ -130,14 +130,16 @@ __device__ __forceinline__ float finite_max(float m) {
 // The global scale of a group whose largest magnitude is m.
 __device__ __forceinline__ float global_of(float m) { return fmaxf(m / kGlobalDiv, kGlobalMin); }
 
-// A quotient a / b from y = 1 / b to a unit or two of its last place: a y,
-// corrected by its residual a - q b (one fma, exact) times y, is the float next
-// to a / b, so that ties of the roundings that follow are where the division
-// puts them (Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990).
-__device__ __forceinline__ f32x2 quotient2(f32x2 a, f32x2 minus_b, f32x2 y) {
-  const f32x2 q = mul2(a, y);
-  return fma2(fma2(q, minus_b, a), y, q);
+// The negative of a quotient a / b from y = 1 / b to a unit or two of its last
+// place: a y, corrected by its residual a - q b (one fma, exact) times y, is the
+// float next to a / b, so that ties of the roundings that follow are where the
+// division puts them (Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990).  The negative, as zeros keep their sign in
+// it: for a = -0, q = -a y = +0, the residual q b + a = +0 and +0 * -y + q = +0; the
+// quotient itself would be +0 + q = +0.
+__device__ __forceinline__ f32x2 minus_quotient2(f32x2 a, f32x2 b, f32x2 minus_y) {
+  const f32x2 q = mul2(a, minus_y);
+  return fma2(fma2(q, b, a), minus_y, q);
 }
 __device__ __forceinline__ float reciprocal(float v) {
   float r;
@@ -170,16 +172,17 @@ __device__ __forceinline__ uint2 block_codes(const RawBlock<T> &r, float s, floa
   f32x2 f[8];
   raw_up<T, kBlock16>(r, f);
   const float y = reciprocal(t);
-  const f32x2 yy = pair(y, y), mt = pair(-t, -t);
+  const f32x2 my = pair(-y, -y), tt = pair(t, t);
   if (m * y < 0x1p60f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = quotient2(f[i], mt, yy);
+    for (int i = 0; i < 8; ++i) f[i] = minus_quotient2(f[i], tt, my);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = mul2(f[i], yy);
+    for (int i = 0; i < 8; ++i) f[i] = mul2(f[i], my);
   }
-  const uint2 c = make_uint2(to_e2m1x8(f), to_e2m1x8(f + 4));
-  return s > 0.f ? c : make_uint2(0u, 0u);
+  constexpr uint32_t kSigns = 0x88888888u;   // of the negative quotients, turned
+  const uint32_t live = s > 0.f ? ~0u : 0u;
+  return make_uint2((to_e2m1x8(f) ^ kSigns) & live, (to_e2m1x8(f + 4) ^ kSigns) & live);
 }
 
 }  // namespace moe

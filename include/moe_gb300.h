@@ -617,7 +617,8 @@ int moe_decode_block(const moe_layer_desc *layer, const uint16_t *x,
  *            neither NaN nor infinity; or as given
  *     s    = e4m3(min(max|block| / (6 g), 448)); NaN for the other blocks
  *     t    = s * g
- *     code = e2m1(x / t), ties to even, at most 6; 0 where s is 0 or NaN
+ *     code = e2m1(x / t), ties to even, at most 6, with x's sign if it is 0
+ *            too; 0 where s is 0 or NaN
  *   and an element's value is code * t.
  * Layout, as moe_proj's NVFP4_G16: codes [groups][rows][cols/2] bytes, element
  * 2i in the low nibble; scale [groups][rows][cols/16] E4M3 bytes; global_scale

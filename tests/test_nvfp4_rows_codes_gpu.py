@@ -1,0 +1,48 @@
+"""Codes of the four-bit quantiser where x is a negative zero: the very bytes of
+the definition
+
+    t = fl(s g),  code = e2m1(fl(x / t)), ties to even, at most 6
+
+whose rounded quotients the restatement takes from float64 divisions (a
+quotient of fp32 numbers rounded to float64 and then to fp32 is the rounded
+quotient).  Every comparison is equality."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import expert_routing_alignment_gb300 as moe
+from tests.test_nvfp4_rows_gpu import ALL, BF, FL, HF, check_quantized, gen, randn, ref_quantize
+
+pytestmark = pytest.mark.gpu
+
+def nibbles(codes):
+    return torch.stack([codes & 15, codes >> 4], -1).flatten(-2)
+
+
+def check_bytes(q, x, given=None):
+    """The codes' own bits, the sign of zeros among them."""
+    code, s, _, _ = ref_quantize(x, given)
+    a = code.abs()
+    want = torch.where(a < 2, 2 * a, torch.where(a < 4, a + 2, a / 2 + 4))
+    live = torch.repeat_interleave(s > 0, 16, -1)
+    want = want + 8.0 * (torch.signbit(x) & live)
+    got = nibbles(q["codes"]).double()
+    bad = got != want
+    assert not bad.any(), (int(bad.sum()), x[bad][:4], got[bad][:4], want[bad][:4])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FL])
+def test_zeros_keep_their_sign(dtype):
+    x = randn(gen(3), 9, 64, dtype=dtype)
+    x[:, ::3] = 0.0
+    x[:, 1::3] = -0.0
+    x[0, 16:32] = -0.0      # a block of zeros alone
+    x[1] = -0.0             # a row of them
+    for shape in ((9, 64), (3, 3, 64)):
+        q = moe.moe_quantize_nvfp4(x.view(shape), want=ALL)
+        check_quantized(q, x.view(shape))
+        check_bytes(q, x.view(shape))
+        v, live = q["values"].view(9, 64), torch.repeat_interleave(
+            q["scale"].view(9, 4).view(torch.float8_e4m3fn).float() > 0, 16, -1)
+        assert torch.equal(torch.signbit(v)[live], torch.signbit(x)[live])
