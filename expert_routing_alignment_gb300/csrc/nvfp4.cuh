@@ -157,7 +157,7 @@ struct GlobalScale {
 // A block's scale byte from its maximum m:
 //   s = e4m3(min(m / (6 g), 448)), NaN for a block with a NaN or an infinity.
 // Quotients over 2^60 (a given scale far below the values) go without the
-// residual, which could leave fp32's range.
+// residual, which could leave fp32's range: their scale is 448 either way.
 __device__ __forceinline__ uint32_t block_scale(float m, const GlobalScale &g) {
   const float q = m * g.inv;
   float r = q < 0x1p60f ? fmaf(fmaf(-q, g.six, m), g.inv, q) : q;
@@ -165,21 +165,36 @@ __device__ __forceinline__ uint32_t block_scale(float m, const GlobalScale &g) {
   return to_e4m3x2(r, 0.f) & 0xFFu;
 }
 
+// Magnitudes above 8 t down to it, where every code is 6.
+template <typename T>
+__device__ __forceinline__ RawBlock<T> clamped(RawBlock<T> r, float t) {
+  if constexpr (sizeof(typename T::bits) == 2) {
+    const uint32_t most = T::down2(8.f * t, 8.f * t);
+#pragma unroll
+    for (int i = 0; i < RawBlock<T>::kWords; ++i)
+      r.w[i] = T::min2(r.w[i] & 0x7FFF7FFFu, most) | (r.w[i] & 0x80008000u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < RawBlock<T>::kWords; ++i)
+      r.w[i] = __float_as_uint(
+          copysignf(fminf(fabsf(__uint_as_float(r.w[i])), 8.f * t), __uint_as_float(r.w[i])));
+  }
+  return r;
+}
+
 // The codes of a block with the step t (its scale s times the global one) and the
 // maximum m: e2m1(x / t), and 0 throughout where s is 0 or NaN.
 template <typename T>
-__device__ __forceinline__ uint2 block_codes(const RawBlock<T> &r, float s, float t, float m) {
-  f32x2 f[8];
-  raw_up<T, kBlock16>(r, f);
+__device__ __forceinline__ uint2 block_codes(RawBlock<T> r, float s, float t, float m) {
   const float y = reciprocal(t);
   const f32x2 my = pair(-y, -y), tt = pair(t, t);
-  if (m * y < 0x1p60f) {
+  // an infinite quotient has no residual (those of fp16 reach 2^88 at most)
+  if constexpr (!std::is_same_v<T, F16>)
+    if (!(m * y < 0x1p126f)) r = clamped<T>(r, t);
+  f32x2 f[8];
+  raw_up<T, kBlock16>(r, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = minus_quotient2(f[i], tt, my);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = mul2(f[i], my);
-  }
+  for (int i = 0; i < 8; ++i) f[i] = minus_quotient2(f[i], tt, my);
   constexpr uint32_t kSigns = 0x88888888u;   // of the negative quotients, turned
   const uint32_t live = s > 0.f ? ~0u : 0u;
   return make_uint2((to_e2m1x8(f) ^ kSigns) & live, (to_e2m1x8(f + 4) ^ kSigns) & live);

@@ -1,5 +1,5 @@
-"""Codes of the four-bit quantiser where x is a negative zero: the very bytes of
-the definition
+"""Codes of the four-bit quantiser where x is a negative zero, and where a block's
+elements are many powers of two apart: the very bytes of the definition
 
     t = fl(s g),  code = e2m1(fl(x / t)), ties to even, at most 6
 
@@ -15,6 +15,9 @@ import expert_routing_alignment_gb300 as moe
 from tests.test_nvfp4_rows_gpu import ALL, BF, FL, HF, check_quantized, gen, randn, ref_quantize
 
 pytestmark = pytest.mark.gpu
+
+BORDERS = (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)
+
 
 def nibbles(codes):
     return torch.stack([codes & 15, codes >> 4], -1).flatten(-2)
@@ -46,3 +49,23 @@ def test_zeros_keep_their_sign(dtype):
         v, live = q["values"].view(9, 64), torch.repeat_interleave(
             q["scale"].view(9, 4).view(torch.float8_e4m3fn).float() > 0, 16, -1)
         assert torch.equal(torch.signbit(v)[live], torch.signbit(x)[live])
+
+
+@pytest.mark.parametrize("dtype", [BF, FL])
+@pytest.mark.parametrize("power", [-30, 20, 53, 55, 60, 127])
+def test_ties_beside_an_element_far_above_the_scale(power, dtype):
+    """Under a given scale far below a block's maximum the codes of its small
+    elements are still the division's."""
+    lanes, given = [], []
+    for k in (*range(16, 37), *range(128, 256, 3)):
+        g = k * 2.0 ** (-84 if k < 128 else -87)
+        t = 448.0 * g           # 11 bits at most, c t 14: exact in fp32
+        row = [2.0 ** power] + [c * t for c in BORDERS] + [-c * t for c in BORDERS] + [-0.0]
+        lanes.append(row)
+        given.append(g)
+    x = torch.tensor(lanes, dtype=torch.float64, device="cuda").to(dtype)
+    given = torch.tensor(given, dtype=torch.float64, device="cuda").float()
+    q = moe.moe_quantize_nvfp4(x, global_scale=given, want=ALL)
+    assert bool((q["scale"] == 0x7E).all())
+    check_quantized(q, x, given)
+    check_bytes(q, x, given)
