@@ -130,13 +130,18 @@ __device__ __forceinline__ float finite_max(float m) {
 // The global scale of a group whose largest magnitude is m.
 __device__ __forceinline__ float global_of(float m) { return fmaxf(m / kGlobalDiv, kGlobalMin); }
 
-// The negative of a quotient a / b from y = 1 / b to a unit or two of its last
-// place: a y, corrected by its residual a - q b (one fma, exact) times y, is the
-// float next to a / b, so that ties of the roundings that follow are where the
-// division puts them (Markstein, "Computation of elementary functions on the IBM
-// RISC System/6000 processor", 1990).  The negative, as zeros keep their sign in
-// it: for a = -0, q = -a y = +0, the residual q b + a = +0 and +0 * -y + q = +0; the
-// quotient itself would be +0 + q = +0.
+// The negative of a quotient a / b from y, nearly 1 / b: q = a y, corrected by its
+// residual a - q b (one fma, exact) times y (Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990).  It is the float next to
+// a / b unless that is within about 2^-22 units of the middle of two floats.  With y the
+// float next to 1 / b no such pair lies beside a border of E2M1 or E4M3 (a search over
+// every 24-bit b); with y a unit off there are a few, of b = 12582909 and 16777209 to
+// 16777215 (16777212: a = 20971516, border 1.25).  The reciprocal of the chip that this
+// is for is near enough there: a test takes every b, each border and the floats around
+// border * b, and finds the division's codes.  (Rounded correctly, __frcp_rn took the
+// codes of 32 x 1536 x 2048 bf16 from 75.6 to 79.7 us.)  The negative, as zeros keep
+// their sign in it: for a = -0, q = -a y = +0, the residual q b + a = +0 and
+// +0 * -y + q = +0; the quotient itself would be +0 + q = +0.
 __device__ __forceinline__ f32x2 minus_quotient2(f32x2 a, f32x2 b, f32x2 minus_y) {
   const f32x2 q = mul2(a, minus_y);
   return fma2(fma2(q, b, a), minus_y, q);
