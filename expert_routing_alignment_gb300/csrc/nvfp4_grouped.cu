@@ -764,9 +764,15 @@ __device__ void copier(const ProductArgs &a, Smem &S) {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// silu(g) * u, from e = e^-|g|: the denominator 1 + e is in [1, 2], where the fast
+// reciprocal is right to a unit, and gates far below zero end where fp32's exponential
+// does.  (g / (1 + e^-g) by the fast division is 0 from -87.3 on, and took the gate and
+// up of 4096 rows 81.0 us instead of 80.1; with e^-64 taken out of far gates 97.)
 __device__ __forceinline__ float silu_times(float g, float u) {
-  // a denominator over 2^126 gives 0, for what is below 2^-119
-  return __fdividef(g, 1.f + expf(-g)) * u;
+  const float e = expf(-fabsf(g));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return (g < 0.f ? g * e : g) * r * u;
 }
 
 template <typename T>
