@@ -1071,11 +1071,12 @@ def moe_grouped_product_nvfp4(weight, rows, tables: dict, top_k: int, M: Optiona
                               stream=None) -> torch.Tensor:
     """out [max_total, R] = each real position's row times its expert's matrix:
     weight (codes [E, R, C / 2], scale, global_scale) and rows (the same of
-    moe_quantize_nvfp4, as its dict or in that order), four bits both.  Without
-    M the rows are the tokens' own, read through the tables; with M, the number
-    of tokens, they are in expert order, [max_total, C].  The tables are those of
-    as many tokens and top_k.  out has out_dtype (bf16 by default); its padding
-    rows stay as they were (undefined in a new buffer)."""
+    moe_quantize_nvfp4, as its dict or in that order), four bits both, under
+    scales without a sign, as the tensor cores take them.  Without M the rows are
+    the tokens' own, read through the tables; with M, the number of tokens, they
+    are in expert order, [max_total, C].  The tables are those of as many tokens
+    and top_k.  out has out_dtype (bf16 by default); its padding rows stay as they
+    were (undefined in a new buffer)."""
     return _grouped_nvfp4("moe_grouped_product_nvfp4", (weight,), rows, tables, top_k, M, out,
                           out_dtype, err_word, stream)
 

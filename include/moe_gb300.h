@@ -653,7 +653,7 @@ int moe_quantize_nvfp4(const void *x, int64_t x_stride, int dtype, int groups,
                        void *stream);
 
 /* The values of codes: out[groups * rows][cols] of type dtype = code * (s * g),
- * rounded once.  Sizes and errors as moe_quantize_nvfp4. */
+ * rounded once (a scale's sign counts).  Sizes and errors as moe_quantize_nvfp4. */
 int moe_dequantize_nvfp4(const uint8_t *codes, const uint8_t *scale,
                          const float *global_scale, int groups, int rows,
                          int cols, int dtype, void *out, void *stream);
@@ -676,6 +676,11 @@ int moe_dequantize_nvfp4(const uint8_t *codes, const uint8_t *scale,
  *   positions are written, all others stay as they were.
  * The product of a gradient with the experts' weights is the same call on a
  * set of the transposed matrices, quantised along the other side.
+ * Scales are E4M3 bytes without a sign (0x00 to 0x7F), as moe_quantize_nvfp4
+ * makes them: the tensor cores take them as UE4M3.  A byte with its highest bit
+ * set has no defined product here, unlike in moe_dequantize_nvfp4 and the
+ * layer's kernels, which honour the sign: clear it and turn the signs of the
+ * block's codes (codes ^ 0x88) first.
  * Any number of rows for each expert; M = 0 is valid.  in_dim: a multiple of 32
  * up to MOE_MAX_ROW_HIDDEN (multiples of 256 are fast), any out_dim up to
  * 4 * MOE_MAX_ROW_HIDDEN.  Deterministic, and a row's bits do not depend on the
