@@ -138,8 +138,8 @@ __device__ __forceinline__ float global_of(float m) { return fmaxf(m / kGlobalDi
 // every 24-bit b); with y a unit off there are a few, of b = 12582909 and 16777209 to
 // 16777215 (16777212: a = 20971516, border 1.25).  The reciprocal of the chip that this
 // is for is near enough there: a test takes every b, each border and the floats around
-// border * b, and finds the division's codes.  (Rounded correctly, __frcp_rn took the
-// codes of 32 x 1536 x 2048 bf16 from 75.6 to 79.7 us.)  The negative, as zeros keep
+// border * b, and finds the division's codes.  (One that is rounded correctly,
+// __frcp_rn, takes 32 x 1536 x 2048 bf16 from 75.6 to 79.7 us.)  The negative, as zeros keep
 // their sign in it: for a = -0, q = -a y = +0, the residual q b + a = +0 and
 // +0 * -y + q = +0; the quotient itself would be +0 + q = +0.
 __device__ __forceinline__ f32x2 minus_quotient2(f32x2 a, f32x2 b, f32x2 minus_y) {

@@ -44,13 +44,17 @@
 // Measured and bounds (one GB300; E experts, k an expert's input width):
 //  * Few rows an expert: HBM.  128 tokens, 199 of 256 experts active, 4096 x 1536
 //    gate and up (1.41 GB read): 205-216 us, 6.6-6.9 TB/s.
-//  * Many: shared memory and the ring.  An MMA of 256 columns and 64 k takes 128
-//    clocks and reads 12 KB of the 128 bytes a clock that shared memory gives, and
-//    the copies write as much: with them a stage takes about 790 clocks instead of
-//    512, and three stages (all that fits) do not hide a copy's 2000.  Gate and up
-//    of 4096 tokens (128 experts, 2048 x 768, 206 GFLOP) 80 us, 2.6 PFLOP/s; down
-//    of 8192 (256 experts, 1536 x 4096, 825 GFLOP, 1.5 GB) 304 us, 2.7.  Two stages
-//    take 359 us there; tiles of 192 columns, whose accumulators tensor memory
+//  * Many: no path's rate, but the ring of three stages (all that fits) and the MMAs'
+//    issue.  Of about 1450 clocks a stage (clock() in the issuing warp; 4096 tokens'
+//    gate and up, and down of 64 experts) 790-890 go by while the stage's copies of
+//    scales and MMAs are given out, whose own time is 512; 350-480 are waited for its
+//    bytes, which are there 2800-3200 clocks after their copies began; 160-290 lie
+//    between tiles (the next tile's rows, the epilogue's taking of the accumulators).
+//    Meanwhile (ncu) L2 to SM carries 10 TB/s, 27 % of what it can, L2 is at 37-44 %,
+//    shared memory's banks at 31-36 %, HBM at 39-49 %, the tensor pipe at 28 %.  Gate
+//    and up of 4096 tokens (128 experts, 2048 x 768, 206 GFLOP) 80 us, 2.6 PFLOP/s;
+//    down of 8192 (256 experts, 1536 x 4096, 825 GFLOP, 1.5 GB) 304-311 us, 2.7.  Two
+//    stages take 359 us there; tiles of 192 columns, whose accumulators tensor memory
 //    holds twice, 365; codes brought to L2 ahead, 333.
 //  * One token: its chain of latencies, 8.3 us (8 experts, 14 MB): 1 us to the
 //    first tile's place, 1 to its first copies, eight stages of 0.45, which the

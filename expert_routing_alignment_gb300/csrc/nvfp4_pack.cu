@@ -11,11 +11,13 @@
 // values took 32.4 us.)  The inverse has pieces of 16 bytes a lane, so that a
 // warp's loads and stores are runs of neighbours.
 // Rows: x is read once; 8192 x 4096 bf16 with values (153 MB) 24.0 us, 6.4 TB/s,
-// bound by HBM and, nearly, by issue.  Matrices: read twice, for the maximum and
-// for the codes; 32 x 1536 x 2048 bf16 with values (459 MB, 660 with the second
-// read) 104 us.  (Read once, held in the shared memory of CTAs that meet at the
-// maximum: 143 us, each meeting 4.5; in turns that find x in L2: no faster.)  The
-// inverse: 64 x 768 x 2048 to bf16 (258 MB) 39.7 us, 6.5 TB/s.
+// bound by HBM and, nearly, by issue; without values (86 MB) 15.8, 5.5 TB/s, as the
+// codes' arithmetic is the same.  Matrices: read twice, for the maximum and for the
+// codes; 32 x 1536 x 2048 bf16 with values (459 MB, 660 with the second read, which
+// finds little of x in L2) 104 us, without 75.  (Read once, held in the shared memory
+// of CTAs that meet at the maximum: 143 us with values, each meeting 4.5; in turns
+// that find x in L2: 111 to 135.)  The inverse: 64 x 768 x 2048 to bf16 (258 MB)
+// 39.7 us, 6.5 TB/s.
 #include "nvfp4.cuh"
 
 namespace moe {
@@ -243,8 +245,12 @@ int most_parts(int groups) {
   const int parts = groups > 0 ? 4096 / groups : 1;
   return parts < 1 ? 1 : parts > 1024 ? 1024 : parts;
 }
-// CTAs of a group: 24 for each SM in all, three times what is resident, so that the
-// last ones are short (32 x 1536 x 2048 bf16 with values 104 us, 8 an SM 110).
+// CTAs of a group: 24 for each SM in all, several times what is resident (8 of the
+// maximum's, 6 of the codes'), so that the last ones are short.  bf16 with values, us by
+// 6, 8, 12, 24 and 48 an SM: 32 x 1536 x 2048 110, 111, 108, 104, 104; 256 x 512 x 768
+// 114, 118, 108, 105, 105; 128 x 2048 x 1536 439, 469, 422, 408, 397.  One matrix has
+// most_parts at most: 16384 x 16384 293 by 912, and 326 by 1024, which is no whole
+// number of waves.
 int group_parts(int groups, int rows, int cols) {
   const int64_t most = ceil_div64((int64_t)rows * (cols / kBlock16), kThreads);
   int64_t parts = (int64_t)sm_count() * 24 / groups;
@@ -293,9 +299,10 @@ extern "C" int moe_quantize_nvfp4(const void *x, int64_t x_stride, int dtype, in
       constexpr int A = decltype(al)::value;
       if (rows == 1) {
         // Two blocks a thread where there are more than the device has threads: the
-        // row's scale and its reciprocal are each thread's own work (8192 x 4096 bf16
-        // with values 24.0 us, one block 27.8, four 23.7); 8 rows take 1.8 us with
-        // one, 2.1 with two.
+        // row's scale and its reciprocal are each thread's own work.  bf16 with values,
+        // us with one and with two: 512 x 2048 2.3 and 2.4, 1024 x 4096 4.8 and 4.5,
+        // 2048 x 4096 7.3 and 5.9, 16384 x 2048 26.8 and 23.9; 8192 x 4096 27.8 and 24.0
+        // (23.7 with four).
         const int want = (int64_t)groups * a.blocks > (int64_t)sm_count() * 2048 ? 2 : 1;
         int tpr = 1;
         while (want * tpr < a.blocks && tpr < kThreads) tpr *= 2;
