@@ -14,7 +14,7 @@
 // bound by HBM and, nearly, by issue; without values (86 MB) 15.8, 5.5 TB/s, as the
 // codes' arithmetic is the same.  Matrices: read twice, for the maximum and for the
 // codes; 32 x 1536 x 2048 bf16 with values (459 MB, 660 with the second read, which
-// finds little of x in L2) 104 us, without 75.  (Read once, held in the shared memory
+// finds nothing of x in L2) 104 us, without 75.  (Read once, held in the shared memory
 // of CTAs that meet at the maximum: 143 us with values, each meeting 4.5; in turns
 // that find x in L2: 111 to 135.)  The inverse: 64 x 768 x 2048 to bf16 (258 MB)
 // 39.7 us, 6.5 TB/s.
