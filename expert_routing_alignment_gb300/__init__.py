@@ -1075,8 +1075,9 @@ def moe_grouped_product_nvfp4(weight, rows, tables: dict, top_k: int, M: Optiona
     scales without a sign, as the tensor cores take them.  Without M the rows are
     the tokens' own, read through the tables; with M, the number of tokens, they
     are in expert order, [max_total, C].  The tables are those of as many tokens
-    and top_k (their "num_slots", or token_to_perm's length without it).  out has out_dtype (bf16 by default); its padding rows stay as they
-    were (undefined in a new buffer)."""
+    and top_k (their "num_slots", or token_to_perm's length without it).  out has
+    out_dtype (bf16 by default); its padding rows stay as they were (undefined in
+    a new buffer)."""
     return _grouped_nvfp4("moe_grouped_product_nvfp4", (weight,), rows, tables, top_k, M, out,
                           out_dtype, err_word, stream)
 
